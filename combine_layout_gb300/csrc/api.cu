@@ -10,6 +10,8 @@
 #include <new>
 
 #include "common.cuh"
+#include "ffn.cuh"
+#include "norm.cuh"
 
 using namespace moeep;
 
@@ -952,6 +954,308 @@ int moe_ep_clear_device_errors(moe_ep_group_t g)
     if (!g) return MOE_EP_ERR_INVALID;
     for (int i = 0; i < kErrSlots; ++i) g->err_host[i] = 0u;
     return MOE_EP_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+inline bool overlap(const void* a, size_t na, const void* b, size_t nb)
+{
+    const char* x = (const char*)a;
+    const char* y = (const char*)b;
+    return a && b && x < y + nb && y < x + na;
+}
+
+// What every feed-forward call on the receive rows checks first: the handle
+// has a layout, the buffers hold its rows, and the width fits TMA's 16-byte
+// strides.
+int check_rows(moe_ep_handle_t h, int width, int64_t recv_rows)
+{
+    if (!h) return MOE_EP_ERR_INVALID;
+    int st = check_group(h->g);
+    if (st != MOE_EP_OK) return st;
+    if (!h->routed || width < 8 || width % 8 != 0 || width > (1 << 24)) return MOE_EP_ERR_INVALID;
+    if (recv_rows < required_rows(h) || recv_rows > INT32_MAX) return MOE_EP_ERR_INVALID;
+    return MOE_EP_OK;
+}
+
+inline size_t row_bytes(int64_t rows, int width) { return (size_t)rows * width * 2; }
+
+RowsArgs rows_args(const moe_ep_handle* h, int M, int K, int F, int act, void* out, void* keep,
+                   const void* gate_up)
+{
+    RowsArgs a;
+    a.cnt = h->cnt;
+    a.off = h->off;
+    a.E = h->g->E;
+    a.S = h->g->S;
+    a.mode = h->g->mode;
+    a.M = M;
+    a.K = K;
+    a.F = F;
+    a.mt = 0;
+    a.act = act;
+    a.out = (__nv_bfloat16*)out;
+    a.keep = (__nv_bfloat16*)keep;
+    a.gate_up = (const __nv_bfloat16*)gate_up;
+    a.err = h->g->err_dev;
+    return a;
+}
+
+int run_rows(moe_ep_handle_t h, int epi, const void* rows_in, int64_t recv_rows, const void* weights,
+             const RowsArgs& a, cudaStream_t s)
+{
+    int st = ensure_counts(h, s);
+    if (st != MOE_EP_OK) return st;
+    return cuda_status(launch_rows_product(epi, rows_in, recv_rows, weights, a, (int64_t)h->T * h->k,
+                                           h->g->sm_count, s));
+}
+
+inline bool valid_act(int act) { return act == MOE_EP_ACT_SILU || act == MOE_EP_ACT_GELU; }
+
+}  // namespace
+
+extern "C" {
+
+int moe_ep_ffn_gate_up(moe_ep_handle_t h, const void* x, const void* w_gate_up, int ffn, int act,
+                       void* hid, void* gate_up, int64_t recv_rows, moe_ep_stream_t stream)
+{
+    int st = check_rows(h, ffn, recv_rows);
+    if (st != MOE_EP_OK) return st;
+    if (!valid_act(act)) return MOE_EP_ERR_INVALID;
+    if (h->T == 0) return MOE_EP_OK;
+    if (!x || !w_gate_up || !hid || !aligned16(x) || !aligned16(w_gate_up) || !aligned16(hid) ||
+        !aligned16(gate_up))
+        return MOE_EP_ERR_INVALID;
+    const int H = h->g->H;
+    const size_t xb = row_bytes(recv_rows, H), hb = row_bytes(recv_rows, ffn);
+    const size_t wb = (size_t)h->g->E * 2 * ffn * H * 2;
+    if (overlap(hid, hb, x, xb) || overlap(hid, hb, w_gate_up, wb) || overlap(gate_up, 2 * hb, x, xb) ||
+        overlap(gate_up, 2 * hb, w_gate_up, wb) || overlap(gate_up, 2 * hb, hid, hb))
+        return MOE_EP_ERR_INVALID;
+    return run_rows(h, kRowsGateUp, x, recv_rows, w_gate_up,
+                    rows_args(h, ffn, H, ffn, act, hid, gate_up, nullptr), (cudaStream_t)stream);
+}
+
+int moe_ep_ffn_down(moe_ep_handle_t h, const void* hid, const void* w_down, int ffn, void* y,
+                    int64_t recv_rows, moe_ep_stream_t stream)
+{
+    int st = check_rows(h, ffn, recv_rows);
+    if (st != MOE_EP_OK) return st;
+    if (h->T == 0) return MOE_EP_OK;
+    if (!hid || !w_down || !y || !aligned16(hid) || !aligned16(w_down) || !aligned16(y))
+        return MOE_EP_ERR_INVALID;
+    const int H = h->g->H;
+    const size_t yb = row_bytes(recv_rows, H);
+    if (overlap(y, yb, hid, row_bytes(recv_rows, ffn)) ||
+        overlap(y, yb, w_down, (size_t)h->g->E * ffn * H * 2))
+        return MOE_EP_ERR_INVALID;
+    return run_rows(h, kRowsStore, hid, recv_rows, w_down,
+                    rows_args(h, H, ffn, ffn, 0, y, nullptr, nullptr), (cudaStream_t)stream);
+}
+
+int moe_ep_ffn_down_backward(moe_ep_handle_t h, const void* dy, const void* w_down,
+                             const void* gate_up, int ffn, int act, void* d_gate_up, void* hid,
+                             int64_t recv_rows, moe_ep_stream_t stream)
+{
+    int st = check_rows(h, ffn, recv_rows);
+    if (st != MOE_EP_OK) return st;
+    if (!valid_act(act)) return MOE_EP_ERR_INVALID;
+    if (h->T == 0) return MOE_EP_OK;
+    if (!dy || !w_down || !gate_up || !d_gate_up || !aligned16(dy) || !aligned16(w_down) ||
+        !aligned16(gate_up) || !aligned16(d_gate_up) || !aligned16(hid))
+        return MOE_EP_ERR_INVALID;
+    const int H = h->g->H;
+    const size_t yb = row_bytes(recv_rows, H), hb = row_bytes(recv_rows, ffn);
+    const size_t wb = (size_t)h->g->E * ffn * H * 2;
+    if (overlap(d_gate_up, 2 * hb, dy, yb) || overlap(d_gate_up, 2 * hb, w_down, wb) ||
+        overlap(d_gate_up, 2 * hb, gate_up, 2 * hb) || overlap(hid, hb, dy, yb) ||
+        overlap(hid, hb, w_down, wb) || overlap(hid, hb, gate_up, 2 * hb) ||
+        overlap(hid, hb, d_gate_up, 2 * hb))
+        return MOE_EP_ERR_INVALID;
+    return run_rows(h, kRowsDownBwd, dy, recv_rows, w_down,
+                    rows_args(h, ffn, H, ffn, act, d_gate_up, hid, gate_up), (cudaStream_t)stream);
+}
+
+int moe_ep_ffn_gate_up_backward(moe_ep_handle_t h, const void* d_gate_up, const void* w_gate_up,
+                                int ffn, void* dx, int64_t recv_rows, moe_ep_stream_t stream)
+{
+    int st = check_rows(h, ffn, recv_rows);
+    if (st != MOE_EP_OK) return st;
+    if (h->T == 0) return MOE_EP_OK;
+    if (!d_gate_up || !w_gate_up || !dx || !aligned16(d_gate_up) || !aligned16(w_gate_up) ||
+        !aligned16(dx))
+        return MOE_EP_ERR_INVALID;
+    const int H = h->g->H;
+    const size_t xb = row_bytes(recv_rows, H);
+    if (overlap(dx, xb, d_gate_up, row_bytes(recv_rows, 2 * ffn)) ||
+        overlap(dx, xb, w_gate_up, (size_t)h->g->E * 2 * ffn * H * 2))
+        return MOE_EP_ERR_INVALID;
+    return run_rows(h, kRowsStoreT, d_gate_up, recv_rows, w_gate_up,
+                    rows_args(h, H, 2 * ffn, ffn, 0, dx, nullptr, nullptr), (cudaStream_t)stream);
+}
+
+int moe_ep_ffn_weight_grad(moe_ep_handle_t h, const void* a, int m, const void* b, int n, void* dw,
+                           int fp32, int accumulate, int64_t recv_rows, moe_ep_stream_t stream)
+{
+    int st = check_rows(h, m, recv_rows);
+    if (st == MOE_EP_OK) st = check_rows(h, n, recv_rows);
+    if (st != MOE_EP_OK) return st;
+    if ((fp32 != 0 && fp32 != 1) || (accumulate != 0 && accumulate != 1) || (accumulate && !fp32))
+        return MOE_EP_ERR_INVALID;
+    if (!dw || !aligned16(dw)) return MOE_EP_ERR_INVALID;
+    const size_t wb = (size_t)h->g->E * m * n * (fp32 ? 4 : 2);
+    cudaStream_t s = (cudaStream_t)stream;
+    if (h->T == 0)  // no rows: no gradient
+        return accumulate ? MOE_EP_OK : cuda_status(cudaMemsetAsync(dw, 0, wb, s));
+    if (!a || !b || !aligned16(a) || !aligned16(b) || overlap(dw, wb, a, row_bytes(recv_rows, m)) ||
+        overlap(dw, wb, b, row_bytes(recv_rows, n)))
+        return MOE_EP_ERR_INVALID;
+    st = ensure_counts(h, s);
+    if (st != MOE_EP_OK) return st;
+    GradArgs ga;
+    ga.cnt = h->cnt;
+    ga.off = h->off;
+    ga.E = h->g->E;
+    ga.S = h->g->S;
+    ga.mode = h->g->mode;
+    ga.M = m;
+    ga.N = n;
+    ga.mt = ga.nt = 0;
+    ga.accumulate = accumulate;
+    ga.dw = dw;
+    ga.err = h->g->err_dev;
+    return cuda_status(launch_weight_grad(a, b, recv_rows, fp32, ga, h->g->sm_count, s));
+}
+
+int moe_ep_combine_backward(moe_ep_handle_t h, const void* dout, const void* y, const float* topk_w,
+                            void* dy, float* dw, int64_t recv_rows, moe_ep_stream_t stream)
+{
+    if (!h) return MOE_EP_ERR_INVALID;
+    int st = check_group(h->g);
+    if (st != MOE_EP_OK) return st;
+    if (!h->routed || recv_rows < required_rows(h)) return MOE_EP_ERR_INVALID;
+    if (h->T == 0) return MOE_EP_OK;
+    if (!dout || !y || !topk_w || !dy || !dw || !aligned16(dout) || !aligned16(y) || !aligned16(dy) ||
+        ((uintptr_t)topk_w & 3u) || ((uintptr_t)dw & 3u))
+        return MOE_EP_ERR_INVALID;
+    const int H = h->g->H;
+    const size_t yb = row_bytes(recv_rows, H), wb = (size_t)h->T * h->k * 4;
+    if (overlap(dy, yb, y, yb) || overlap(dy, yb, dout, row_bytes(h->T, H)) ||
+        overlap(dy, yb, topk_w, wb) || overlap(dy, yb, dw, wb) || overlap(dw, wb, topk_w, wb) ||
+        overlap(dw, wb, y, yb) || overlap(dw, wb, dout, row_bytes(h->T, H)))
+        return MOE_EP_ERR_INVALID;
+    cudaStream_t s = (cudaStream_t)stream;
+    st = ensure_rows(h, s);
+    if (st != MOE_EP_OK) return st;
+    return cuda_status(launch_combine_bwd(dout, y, h->T, H, h->k, h->row, topk_w, dy, dw, s));
+}
+
+}  // extern "C"
+
+namespace {
+
+// The forward arguments of the norms, checked; MOE_EP_OK and *a filled in, or
+// the error.
+int norm_args(moe_ep_group_t g, const void* o, const void* res, const float* w_post, const float* gate,
+              int gate_per_token, const float* w_pre, float res_scale, float eps, int T, NormArgs* a)
+{
+    int st = check_group(g);
+    if (st != MOE_EP_OK) return st;
+    if (T < 0 || g->H > kMaxNormWidth || !(eps >= 0.f) || (gate_per_token != 0 && gate_per_token != 1))
+        return MOE_EP_ERR_INVALID;
+    if (T > 0 && !o && !res) return MOE_EP_ERR_INVALID;
+    if (T > 0 && !o && (w_post || gate)) return MOE_EP_ERR_INVALID;
+    if (!aligned16(o) || !aligned16(res) || !aligned16(w_post) || !aligned16(w_pre) ||
+        (gate_per_token ? ((uintptr_t)gate & 3u) != 0 : !aligned16(gate)))
+        return MOE_EP_ERR_INVALID;
+    a->o = (const uint4*)o;
+    a->res = (const uint4*)res;
+    a->w_post = w_post;
+    a->gate = gate;
+    a->w_pre = w_pre;
+    a->res_out = nullptr;
+    a->y = nullptr;
+    a->H = g->H;
+    a->per_token = gate_per_token;
+    a->scale = res_scale;
+    a->eps = eps;
+    a->inv_h = 1.f / (float)g->H;
+    return MOE_EP_OK;
+}
+
+// Whether `out` lies on one of the n inputs without being the same buffer.
+bool partly_over(const void* out, const void* const* in, int n, size_t bytes)
+{
+    for (int i = 0; i < n; ++i)
+        if (out != in[i] && overlap(out, bytes, in[i], bytes)) return true;
+    return false;
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_ep_norm_residual(moe_ep_group_t g, const void* o, const void* res, const float* w_post,
+                         const float* gate, int gate_per_token, const float* w_pre, float res_scale,
+                         float eps, int num_tokens, void* res_out, void* y, moe_ep_stream_t stream)
+{
+    NormArgs a;
+    int st = norm_args(g, o, res, w_post, gate, gate_per_token, w_pre, res_scale, eps, num_tokens, &a);
+    if (st != MOE_EP_OK) return st;
+    if (num_tokens == 0) return MOE_EP_OK;
+    if ((!res_out && !y) || (y && !w_pre) || !aligned16(res_out) || !aligned16(y))
+        return MOE_EP_ERR_INVALID;
+    const size_t nb = row_bytes(num_tokens, g->H);
+    const void* in[2] = {o, res};
+    if (partly_over(res_out, in, 2, nb) || partly_over(y, in, 2, nb) || overlap(res_out, nb, y, nb))
+        return MOE_EP_ERR_INVALID;
+    a.res_out = (uint4*)res_out;
+    a.y = (uint4*)y;
+    return cuda_status(launch_norm(a, num_tokens, (cudaStream_t)stream));
+}
+
+int moe_ep_norm_work_floats(moe_ep_group_t g, int64_t* floats)
+{
+    if (!g || !floats) return MOE_EP_ERR_INVALID;
+    *floats = (int64_t)g->sm_count * 3 * g->H;
+    return MOE_EP_OK;
+}
+
+int moe_ep_norm_residual_backward(moe_ep_group_t g, const void* o, const void* res,
+                                  const float* w_post, const float* gate, int gate_per_token,
+                                  const float* w_pre, float res_scale, float eps, int num_tokens,
+                                  const void* dr, const void* dy, void* d_o, void* dres,
+                                  float* dw_post, float* dgate, float* dw_pre, float* work,
+                                  moe_ep_stream_t stream)
+{
+    NormBwdArgs b;
+    int st = norm_args(g, o, res, w_post, gate, gate_per_token, w_pre, res_scale, eps, num_tokens,
+                       &b.f);
+    if (st != MOE_EP_OK) return st;
+    if ((dw_post && !w_post) || (dgate && !gate) || (dw_pre && !w_pre)) return MOE_EP_ERR_INVALID;
+    if (((uintptr_t)dw_post & 3u) || ((uintptr_t)dgate & 3u) || ((uintptr_t)dw_pre & 3u))
+        return MOE_EP_ERR_INVALID;
+    if (num_tokens > 0) {
+        if ((!dr && !dy) || (dy && !w_pre) || (d_o && !o) || (dres && !res) || !work ||
+            !aligned16(work) || !aligned16(dr) || !aligned16(dy) || !aligned16(d_o) ||
+            !aligned16(dres))
+            return MOE_EP_ERR_INVALID;
+        const size_t nb = row_bytes(num_tokens, g->H);
+        const void* in[4] = {o, res, dr, dy};
+        if (partly_over(d_o, in, 4, nb) || partly_over(dres, in, 4, nb) || overlap(d_o, nb, dres, nb))
+            return MOE_EP_ERR_INVALID;
+    }
+    b.dr = (const uint4*)dr;
+    b.dy = (const uint4*)dy;
+    b.d_o = (uint4*)d_o;
+    b.dres = (uint4*)dres;
+    b.dgate = gate_per_token ? dgate : nullptr;
+    b.work = work;
+    b.T = num_tokens;
+    return cuda_status(launch_norm_bwd(b, dw_pre, dw_post, gate_per_token ? nullptr : dgate,
+                                       g->sm_count, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -308,6 +308,11 @@ cudaError_t launch_combine(const void* y, int T, int H, int k, const int32_t* ro
                            void* out, int sm_count, cudaStream_t s,
                            const SendSignal& sig = SendSignal{});
 
+// Backward of the combine: dy[row[t][j]] = bf16(w[t][j] * dout[t]) and
+// dw[t][j] = <dout[t], y[row[t][j]]> (0 for a pair without a row).
+cudaError_t launch_combine_bwd(const void* dout, const void* y, int T, int H, int k, const int32_t* row,
+                               const float* w, void* dy, float* dw, cudaStream_t s);
+
 // Receive side of a send-only operation: one thread waits (at most limit_ns,
 // and a bounded number of polls) until *signal >= expected, then subtracts
 // expected; when the bound passes first it latches err[kErrTimeout].

@@ -21,6 +21,7 @@ MOE_EP_LL, MOE_EP_HT = 0, 1
 (MOE_EP_OK, MOE_EP_ERR_INVALID, MOE_EP_ERR_OVERFLOW, MOE_EP_ERR_CUDA, MOE_EP_ERR_DEVICE,
  MOE_EP_ERR_TIMEOUT) = range(6)
 MOE_EP_W_SOFTMAX_TOPK, MOE_EP_W_SOFTMAX_RENORM, MOE_EP_W_SCORE_NORM = 0, 1, 2
+MOE_EP_ACT_SILU, MOE_EP_ACT_GELU = 0, 1
 MOE_EP_DEVERR_EXPERT_RANGE, MOE_EP_DEVERR_DUPLICATE, MOE_EP_DEVERR_TIMEOUT = 1, 2, 4
 
 
@@ -41,7 +42,7 @@ def _load() -> ctypes.CDLL:
         raise ImportError(f"libmoeep is not built ({LIB_PATH} missing); run "
                           "`python -c 'import __graft_entry__ as g; g.build()'` first")
     lib = ctypes.CDLL(LIB_PATH)
-    P, I, I64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
+    P, I, I64, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float
     PP = ctypes.POINTER(ctypes.c_void_p)
     sig = {
         "moe_ep_create_group": [PP, I, I, I, I, I],
@@ -69,6 +70,15 @@ def _load() -> ctypes.CDLL:
         "moe_ep_dispatch_dedup": [P, P, I, P, P, P, P, P, P, I64, P],
         "moe_ep_expand": [P, P, P, P, P, I, P, P, P, I64, P],
         "moe_ep_combine_dedup": [P, P, P, P, P, P, I64, I64, P],
+        "moe_ep_ffn_gate_up": [P, P, P, I, I, P, P, I64, P],
+        "moe_ep_ffn_down": [P, P, P, I, P, I64, P],
+        "moe_ep_ffn_down_backward": [P, P, P, P, I, I, P, P, I64, P],
+        "moe_ep_ffn_gate_up_backward": [P, P, P, I, P, I64, P],
+        "moe_ep_ffn_weight_grad": [P, P, I, P, I, P, I, I, I64, P],
+        "moe_ep_combine_backward": [P, P, P, P, P, P, I64, P],
+        "moe_ep_norm_residual": [P, P, P, P, P, I, P, F, F, I, P, P, P],
+        "moe_ep_norm_work_floats": [P, ctypes.POINTER(ctypes.c_int64)],
+        "moe_ep_norm_residual_backward": [P, P, P, P, P, I, P, F, F, I, P, P, P, P, P, P, P, P, P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -114,27 +124,36 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+# Experts and hidden of each live group and handle: what the tensors of the
+# expert block's calls are checked against.
+_sizes: dict[int, tuple[int, int]] = {}
+
+
 # ------------------------------------------------------------------ entry points
 def moe_ep_create_group(mode: int, experts: int, ranks: int, max_tokens: int, hidden: int) -> int:
     out = ctypes.c_void_p()
     _check("moe_ep_create_group",
            _lib.moe_ep_create_group(ctypes.byref(out), mode, experts, ranks, max_tokens, hidden))
+    _sizes[out.value] = (experts, hidden)
     return out.value
 
 
 def moe_ep_destroy_group(group: int) -> None:
     _check("moe_ep_destroy_group", _lib.moe_ep_destroy_group(ctypes.c_void_p(group)))
+    _sizes.pop(group, None)
 
 
 def moe_ep_create_handle(group: int, max_topk: int) -> int:
     out = ctypes.c_void_p()
     _check("moe_ep_create_handle",
            _lib.moe_ep_create_handle(ctypes.c_void_p(group), max_topk, ctypes.byref(out)))
+    _sizes[out.value] = _sizes[group]
     return out.value
 
 
 def moe_ep_destroy_handle(handle: int) -> None:
     _check("moe_ep_destroy_handle", _lib.moe_ep_destroy_handle(ctypes.c_void_p(handle)))
+    _sizes.pop(handle, None)
 
 
 def moe_ep_route(handle: int, scores, num_tokens: int, topk: int, topk_idx, topk_w=None,
@@ -282,6 +301,178 @@ def moe_ep_combine_dedup(handle: int, y, topk_w, drecv_src, partial, out,
            _lib.moe_ep_combine_dedup(ctypes.c_void_p(handle), _ptr(y), _ptr(topk_w),
                                      _ptr(drecv_src), _ptr(partial), _ptr(out), recv_rows,
                                      drecv_rows, _stream(stream)))
+
+
+def _typed(dtype, **tensors) -> None:
+    """The calls below read their sizes off the tensors, so their types count."""
+    for name, t in tensors.items():
+        if t is not None and t.dtype != dtype:
+            raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+
+
+def _rows(recv_rows, *tensors) -> int:
+    """Receive rows that every given row tensor holds."""
+    held = min(t.shape[0] for t in tensors if t is not None)
+    return held if recv_rows is None else min(int(recv_rows), held)
+
+
+def _shaped(name, t, *shape) -> None:
+    if t is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+
+
+def moe_ep_ffn_gate_up(handle: int, x, w_gate_up, hid, gate_up=None, act: int = MOE_EP_ACT_SILU,
+                       recv_rows: int | None = None, stream=None) -> None:
+    """x [rows][H], w_gate_up [E][2F][H], hid [rows][F], gate_up [rows][2F] or None."""
+    _typed(torch.bfloat16, x=x, w_gate_up=w_gate_up, hid=hid, gate_up=gate_up)
+    E, H = _sizes[handle]
+    F = hid.shape[1]
+    _shaped("x", x, x.shape[0], H)
+    _shaped("w_gate_up", w_gate_up, E, 2 * F, H)
+    if gate_up is not None:
+        _shaped("gate_up", gate_up, gate_up.shape[0], 2 * F)
+    _check("moe_ep_ffn_gate_up",
+           _lib.moe_ep_ffn_gate_up(ctypes.c_void_p(handle), _ptr(x), _ptr(w_gate_up), F, act,
+                                   _ptr(hid), _ptr(gate_up), _rows(recv_rows, x, hid, gate_up),
+                                   _stream(stream)))
+
+
+def moe_ep_ffn_down(handle: int, hid, w_down, y, recv_rows: int | None = None, stream=None) -> None:
+    """hid [rows][F], w_down [E][H][F], y [rows][H]."""
+    _typed(torch.bfloat16, hid=hid, w_down=w_down, y=y)
+    E, H = _sizes[handle]
+    F = hid.shape[1]
+    _shaped("y", y, y.shape[0], H)
+    _shaped("w_down", w_down, E, H, F)
+    _check("moe_ep_ffn_down",
+           _lib.moe_ep_ffn_down(ctypes.c_void_p(handle), _ptr(hid), _ptr(w_down), F, _ptr(y),
+                                _rows(recv_rows, hid, y), _stream(stream)))
+
+
+def moe_ep_ffn_down_backward(handle: int, dy, w_down, gate_up, d_gate_up, hid=None,
+                             act: int = MOE_EP_ACT_SILU, recv_rows: int | None = None,
+                             stream=None) -> None:
+    """dy [rows][H], w_down [E][H][F], gate_up and d_gate_up [rows][2F], hid [rows][F] or None."""
+    _typed(torch.bfloat16, dy=dy, w_down=w_down, gate_up=gate_up, d_gate_up=d_gate_up, hid=hid)
+    E, H = _sizes[handle]
+    F = w_down.shape[2]
+    _shaped("dy", dy, dy.shape[0], H)
+    _shaped("w_down", w_down, E, H, F)
+    _shaped("gate_up", gate_up, gate_up.shape[0], 2 * F)
+    _shaped("d_gate_up", d_gate_up, d_gate_up.shape[0], 2 * F)
+    if hid is not None:
+        _shaped("hid", hid, hid.shape[0], F)
+    _check("moe_ep_ffn_down_backward",
+           _lib.moe_ep_ffn_down_backward(ctypes.c_void_p(handle), _ptr(dy), _ptr(w_down),
+                                         _ptr(gate_up), F, act, _ptr(d_gate_up), _ptr(hid),
+                                         _rows(recv_rows, dy, gate_up, d_gate_up, hid),
+                                         _stream(stream)))
+
+
+def moe_ep_ffn_gate_up_backward(handle: int, d_gate_up, w_gate_up, dx,
+                                recv_rows: int | None = None, stream=None) -> None:
+    """d_gate_up [rows][2F], w_gate_up [E][2F][H], dx [rows][H]."""
+    _typed(torch.bfloat16, d_gate_up=d_gate_up, w_gate_up=w_gate_up, dx=dx)
+    E, H = _sizes[handle]
+    F2 = d_gate_up.shape[1]
+    _shaped("dx", dx, dx.shape[0], H)
+    _shaped("w_gate_up", w_gate_up, E, F2, H)
+    if F2 % 2:
+        raise ValueError("d_gate_up: gate and up columns expected")
+    _check("moe_ep_ffn_gate_up_backward",
+           _lib.moe_ep_ffn_gate_up_backward(ctypes.c_void_p(handle), _ptr(d_gate_up),
+                                            _ptr(w_gate_up), F2 // 2, _ptr(dx),
+                                            _rows(recv_rows, d_gate_up, dx), _stream(stream)))
+
+
+def moe_ep_ffn_weight_grad(handle: int, a, b, dw, accumulate: bool = False,
+                           recv_rows: int | None = None, stream=None) -> None:
+    """a [rows][m], b [rows][n] bf16, dw [E][m][n] bf16 or fp32."""
+    _typed(torch.bfloat16, a=a, b=b)
+    if dw.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"dw: expected bf16 or fp32, got {dw.dtype}")
+    _shaped("dw", dw, _sizes[handle][0], a.shape[1], b.shape[1])
+    _check("moe_ep_ffn_weight_grad",
+           _lib.moe_ep_ffn_weight_grad(ctypes.c_void_p(handle), _ptr(a), a.shape[1], _ptr(b),
+                                       b.shape[1], _ptr(dw), int(dw.dtype == torch.float32),
+                                       int(bool(accumulate)), _rows(recv_rows, a, b),
+                                       _stream(stream)))
+
+
+def moe_ep_combine_backward(handle: int, dout, y, topk_w, dy, dw, recv_rows: int | None = None,
+                            stream=None) -> None:
+    """dout [T][H], y and dy [rows][H] bf16, topk_w and dw [T][k] fp32."""
+    _typed(torch.bfloat16, dout=dout, y=y, dy=dy)
+    _typed(torch.float32, topk_w=topk_w, dw=dw)
+    H = _sizes[handle][1]
+    for name, t in (("dout", dout), ("y", y), ("dy", dy)):
+        _shaped(name, t, t.shape[0], H)
+    _shaped("dw", dw, *topk_w.shape)
+    _check("moe_ep_combine_backward",
+           _lib.moe_ep_combine_backward(ctypes.c_void_p(handle), _ptr(dout), _ptr(y), _ptr(topk_w),
+                                        _ptr(dy), _ptr(dw), _rows(recv_rows, y, dy),
+                                        _stream(stream)))
+
+
+def _norm_sizes(group, num_tokens, per_token, tokens: dict, channels: dict, gates: dict) -> int:
+    """The number of tokens, after checking every given tensor's shape against it and H."""
+    H = _sizes[group][1]
+    T = num_tokens
+    if T is None:
+        T = next((t.shape[0] for t in tokens.values() if t is not None), 0)
+    for name, t in tokens.items():
+        if t is not None and (t.dim() != 2 or t.shape[0] < T or t.shape[1] != H):
+            raise ValueError(f"{name}: expected [{T}][{H}], got {tuple(t.shape)}")
+    for name, t in channels.items():
+        _shaped(name, t, H)
+    for name, t in gates.items():
+        if t is not None and t.numel() < (T if per_token else H):
+            raise ValueError(f"{name}: expected {T if per_token else H} values, got {t.numel()}")
+    return T
+
+
+def moe_ep_norm_residual(group: int, o, res, w_post, gate, w_pre, res_out, y,
+                         res_scale: float = 1.0, gate_per_token: bool = False, eps: float = 1e-6,
+                         num_tokens: int | None = None, stream=None) -> None:
+    """o, res, res_out, y [T][H] bf16, w_post, w_pre [H] and gate [H] or [T] fp32; None for absent."""
+    _typed(torch.bfloat16, o=o, res=res, res_out=res_out, y=y)
+    _typed(torch.float32, w_post=w_post, gate=gate, w_pre=w_pre)
+    T = _norm_sizes(group, num_tokens, gate_per_token, dict(o=o, res=res, res_out=res_out, y=y),
+                    dict(w_post=w_post, w_pre=w_pre), dict(gate=gate))
+    _check("moe_ep_norm_residual",
+           _lib.moe_ep_norm_residual(ctypes.c_void_p(group), _ptr(o), _ptr(res), _ptr(w_post),
+                                     _ptr(gate), int(bool(gate_per_token)), _ptr(w_pre), res_scale,
+                                     eps, T, _ptr(res_out), _ptr(y), _stream(stream)))
+
+
+def moe_ep_norm_work_floats(group: int) -> int:
+    n = ctypes.c_int64()
+    _check("moe_ep_norm_work_floats",
+           _lib.moe_ep_norm_work_floats(ctypes.c_void_p(group), ctypes.byref(n)))
+    return n.value
+
+
+def moe_ep_norm_residual_backward(group: int, o, res, w_post, gate, w_pre, dr, dy, d_o, dres,
+                                  dw_post, dgate, dw_pre, work, res_scale: float = 1.0,
+                                  gate_per_token: bool = False, eps: float = 1e-6,
+                                  num_tokens: int | None = None, stream=None) -> None:
+    """dr, dy, d_o, dres [T][H] bf16, dw_post, dw_pre [H] and dgate (as gate) fp32, work
+    [moe_ep_norm_work_floats] fp32; None for absent."""
+    _typed(torch.bfloat16, o=o, res=res, dr=dr, dy=dy, d_o=d_o, dres=dres)
+    _typed(torch.float32, w_post=w_post, gate=gate, w_pre=w_pre, dw_post=dw_post, dgate=dgate,
+           dw_pre=dw_pre, work=work)
+    T = _norm_sizes(group, num_tokens, gate_per_token,
+                    dict(o=o, res=res, dr=dr, dy=dy, d_o=d_o, dres=dres),
+                    dict(w_post=w_post, w_pre=w_pre, dw_post=dw_post, dw_pre=dw_pre),
+                    dict(gate=gate, dgate=dgate))
+    if work is not None and work.numel() < moe_ep_norm_work_floats(group):
+        raise ValueError("work: too small (moe_ep_norm_work_floats)")
+    _check("moe_ep_norm_residual_backward",
+           _lib.moe_ep_norm_residual_backward(ctypes.c_void_p(group), _ptr(o), _ptr(res),
+                                              _ptr(w_post), _ptr(gate), int(bool(gate_per_token)),
+                                              _ptr(w_pre), res_scale, eps, T, _ptr(dr), _ptr(dy),
+                                              _ptr(d_o), _ptr(dres), _ptr(dw_post), _ptr(dgate),
+                                              _ptr(dw_pre), _ptr(work), _stream(stream)))
 
 
 def moe_ep_get_device_errors(group: int) -> int:

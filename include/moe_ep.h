@@ -415,6 +415,131 @@ MOE_EP_API int moe_ep_route_layout_static(const float* scores, int num_tokens, i
                                           float* topk_w, int32_t* row, int32_t* cnt, int32_t* off,
                                           int32_t* rcnt, int32_t* roff, moe_ep_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * The expert block around dispatch and combine: the experts' gated feed-forward
+ * over the receive rows, its backward pass and the combine's, and the norms
+ * after and before a block.  The source pages stop at the communication ("NCCL
+ * EP 论文解读", "Tensor Layouts": the expert-major layout is fed to the experts'
+ * GEMM directly); these calls take the layout from there.
+ *
+ * The feed-forward calls work on the rows the last moe_ep_route's layout
+ * defines (HT: each expert's block without its padding; LL: the slots below
+ * each expert's count), read the counts on the device (no host
+ * synchronisation, so they can be captured into a CUDA graph like the
+ * dispatch), and leave every other row of their outputs untouched; rows the
+ * layout does not define may hold anything, NaN included.  Row tensors are
+ * bf16 [recv_rows][width] with recv_rows as for moe_ep_dispatch; weights are
+ * bf16, one matrix per expert, [out][in] row-major.  ffn is the experts'
+ * intermediate width F, a multiple of 8.  All tensors are 16-byte aligned and
+ * an output must not overlap an input or the other output.  Products and sums
+ * are fp32; each output is rounded once to its type.  Errors:
+ * MOE_EP_ERR_INVALID for these and for no preceding moe_ep_route.  Their
+ * waits (on TMA copies and tensor-core work of the same kernel) are bounded
+ * and latch MOE_EP_DEVERR_TIMEOUT. */
+typedef enum {
+    MOE_EP_ACT_SILU = 0, /* g / (1 + exp(-g)) */
+    MOE_EP_ACT_GELU = 1  /* g / 2 (1 + erf(g / sqrt(2))) */
+} moe_ep_act_t;
+
+/* Gate and up projections, activation and product in one kernel:
+ *   g = Wg[e] x, u = Wu[e] x, hid = bf16_rn(act(g) * u)   (g, u not rounded).
+ * x         device bf16 [recv_rows][H], the bf16 receive rows.
+ * w_gate_up device bf16 [E][2F][H]: an expert's F gate rows, then its F up rows.
+ * hid       device bf16 [recv_rows][F].
+ * gate_up   device bf16 [recv_rows][2F] or NULL: g and u, kept for the
+ *           backward pass. */
+MOE_EP_API int moe_ep_ffn_gate_up(moe_ep_handle_t h, const void* x, const void* w_gate_up, int ffn,
+                                  int act, void* hid, void* gate_up, int64_t recv_rows,
+                                  moe_ep_stream_t stream);
+
+/* Down projection: y = Wd[e] hid.  w_down device bf16 [E][H][F]; y device bf16
+ * [recv_rows][H], the rows moe_ep_combine takes. */
+MOE_EP_API int moe_ep_ffn_down(moe_ep_handle_t h, const void* hid, const void* w_down, int ffn,
+                               void* y, int64_t recv_rows, moe_ep_stream_t stream);
+
+/* Backward of the down projection and the activation:
+ *   dh = Wd[e]^T dy, dg = dh * u * act'(g), du = dh * act(g).
+ * dy        device bf16 [recv_rows][H] (moe_ep_combine_backward writes it).
+ * gate_up   device bf16 [recv_rows][2F], kept by moe_ep_ffn_gate_up.
+ * d_gate_up device bf16 [recv_rows][2F]: dg, then du.
+ * hid       device bf16 [recv_rows][F] or NULL: act(g) * u again (from the kept
+ *           g and u), the operand of the down projection's weight gradient --
+ *           so hid need not be kept from the forward pass. */
+MOE_EP_API int moe_ep_ffn_down_backward(moe_ep_handle_t h, const void* dy, const void* w_down,
+                                        const void* gate_up, int ffn, int act, void* d_gate_up,
+                                        void* hid, int64_t recv_rows, moe_ep_stream_t stream);
+
+/* Backward of the gate and up projections: dx = Wg[e]^T dg + Wu[e]^T du, device
+ * bf16 [recv_rows][H].  moe_ep_combine of dx with weights 1 is the dispatch's
+ * backward pass. */
+MOE_EP_API int moe_ep_ffn_gate_up_backward(moe_ep_handle_t h, const void* d_gate_up,
+                                           const void* w_gate_up, int ffn, void* dx,
+                                           int64_t recv_rows, moe_ep_stream_t stream);
+
+/* Weight gradients: dw[e] = sum over expert e's rows of a_row b_row^T, zero for
+ * an expert without rows.
+ * a, b       device bf16 [recv_rows][m] and [recv_rows][n]; m, n multiples of 8.
+ *            (d_gate_up, x) gives the gradient of w_gate_up, (dy, hid) of w_down.
+ * dw         device [E][m][n], bf16 (fp32 == 0) or fp32 (fp32 == 1).
+ * accumulate 1: added to dw (fp32 only); 0: dw is overwritten. */
+MOE_EP_API int moe_ep_ffn_weight_grad(moe_ep_handle_t h, const void* a, int m, const void* b, int n,
+                                      void* dw, int fp32, int accumulate, int64_t recv_rows,
+                                      moe_ep_stream_t stream);
+
+/* Backward of moe_ep_combine: for every pair with a row
+ *   dy[row(t, j)] = bf16_rn(topk_w[t][j] * dout[t]),
+ *   dw[t][j] = sum over h of dout[t][h] * y[row(t, j)][h]   (fp32),
+ * and dw[t][j] = 0 for a pair without one.  Rows of dy that no pair names are
+ * left untouched.
+ * dout device bf16 [T][H]; y the combine's input, dy its gradient, device bf16
+ * [recv_rows][H]; topk_w, dw device fp32 [T][k].  dy must not overlap y or
+ * dout. */
+MOE_EP_API int moe_ep_combine_backward(moe_ep_handle_t h, const void* dout, const void* y,
+                                       const float* topk_w, void* dy, float* dw, int64_t recv_rows,
+                                       moe_ep_stream_t stream);
+
+/* The norms after and before a block with the block's gate and residual scale:
+ *   u = w_post * o / sqrt(mean(o^2) + eps)        (u = o when w_post is NULL)
+ *   r = res_scale * res + gate * u                (gate 1 when NULL)
+ *   y = w_pre * r / sqrt(mean(r^2) + eps)
+ * over rows of H = the group's hidden (at most 16384), computed in fp32 from the
+ * unrounded r, res_out = bf16_rn(r), y = bf16_rn(y).
+ * o       device bf16 [num_tokens][H], the block's output (moe_ep_combine's
+ *         out), or NULL: r = res_scale * res (the norm before the first block).
+ * res     device bf16 [num_tokens][H], the residual stream, or NULL (then o is
+ *         needed): r = gate * u.
+ * w_post, w_pre  device fp32 [H]; w_post needs o, w_pre comes with y.
+ * gate    device fp32 [H], or [num_tokens] with gate_per_token = 1, or NULL.
+ * res_out, y     device bf16 [num_tokens][H]; either may be NULL, not both.  An
+ *         output may be the same buffer as o or res, but not overlap one
+ *         otherwise.
+ * eps must not be negative.  Any num_tokens >= 0.  Asynchronous on `stream`. */
+MOE_EP_API int moe_ep_norm_residual(moe_ep_group_t g, const void* o, const void* res,
+                                    const float* w_post, const float* gate, int gate_per_token,
+                                    const float* w_pre, float res_scale, float eps, int num_tokens,
+                                    void* res_out, void* y, moe_ep_stream_t stream);
+
+/* Floats of workspace moe_ep_norm_residual_backward needs (owned by the
+ * caller; calls that may overlap on the GPU need one each). */
+MOE_EP_API int moe_ep_norm_work_floats(moe_ep_group_t g, int64_t* floats);
+
+/* Backward of moe_ep_norm_residual, its statistics computed again from o and
+ * res (eps and res_scale are constants).
+ * dr, dy  device bf16 [num_tokens][H]: the gradients of res_out and y; either
+ *         may be NULL (zero), not both; dy needs w_pre.
+ * d_o, dres  device bf16 [num_tokens][H], each may be NULL.
+ * dw_post, dw_pre  device fp32 [H], dgate device fp32 of gate's shape; each may
+ *         be NULL, is overwritten (zero for num_tokens = 0), and needs its
+ *         forward argument.  Sums over tokens are taken in a fixed order.
+ * work    device fp32 [moe_ep_norm_work_floats], 16-byte aligned. */
+MOE_EP_API int moe_ep_norm_residual_backward(moe_ep_group_t g, const void* o, const void* res,
+                                             const float* w_post, const float* gate,
+                                             int gate_per_token, const float* w_pre,
+                                             float res_scale, float eps, int num_tokens,
+                                             const void* dr, const void* dy, void* d_o, void* dres,
+                                             float* dw_post, float* dgate, float* dw_pre,
+                                             float* work, moe_ep_stream_t stream);
+
 /* Read (host, no synchronisation) / clear the group's device-error word. */
 MOE_EP_API int moe_ep_get_device_errors(moe_ep_group_t g, uint32_t* bits);
 MOE_EP_API int moe_ep_clear_device_errors(moe_ep_group_t g);
