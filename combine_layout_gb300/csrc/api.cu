@@ -1219,7 +1219,7 @@ int moe_ep_norm_residual(moe_ep_group_t g, const void* o, const void* res, const
 int moe_ep_norm_work_floats(moe_ep_group_t g, int64_t* floats)
 {
     if (!g || !floats) return MOE_EP_ERR_INVALID;
-    *floats = (int64_t)g->sm_count * 3 * g->H;
+    *floats = (int64_t)g->sm_count * norm_ctas(g->H) * 2 * g->H;
     return MOE_EP_OK;
 }
 
@@ -1254,6 +1254,7 @@ int moe_ep_norm_residual_backward(moe_ep_group_t g, const void* o, const void* r
     b.dgate = gate_per_token ? dgate : nullptr;
     b.work = work;
     b.T = num_tokens;
+    b.err = g->err_dev;
     return cuda_status(launch_norm_bwd(b, dw_pre, dw_post, gate_per_token ? nullptr : dgate,
                                        g->sm_count, (cudaStream_t)stream));
 }

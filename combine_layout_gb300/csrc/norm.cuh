@@ -9,6 +9,9 @@ namespace moeep {
 // Widest row the norms take: two vectors of 8 for each of 1024 threads.
 constexpr int kMaxNormWidth = 16384;
 
+// CTAs per SM of the persistent kernels: narrow rows need few threads each.
+inline int norm_ctas(int H) { return H >= 4096 ? 1 : H >= 2048 ? 2 : H >= 1024 ? 4 : 8; }
+
 struct NormArgs {
     const uint4* o;       // bf16 [T][H] (may be null)
     const uint4* res;     // bf16 [T][H] (may be null)
@@ -29,8 +32,9 @@ struct NormBwdArgs {
     uint4* d_o;        // (may be null)
     uint4* dres;       // (may be null)
     float* dgate;      // [T]: the per-token gate's gradient (may be null)
-    float* work;       // [CTAs][3][H]
+    float* work;       // [CTAs][2][H]
     int T;
+    unsigned* err;
 };
 cudaError_t launch_norm_bwd(const NormBwdArgs& b, float* dw_pre, float* dw_post, float* dgate_channel,
                             int sm_count, cudaStream_t s);

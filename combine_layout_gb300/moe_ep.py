@@ -303,146 +303,169 @@ def moe_ep_combine_dedup(handle: int, y, topk_w, drecv_src, partial, out,
                                      drecv_rows, _stream(stream)))
 
 
-def _typed(dtype, **tensors) -> None:
-    """The calls below read their sizes off the tensors, so their types count."""
-    for name, t in tensors.items():
-        if t is not None and t.dtype != dtype:
-            raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+# The expert block's calls are made per layer and step, often on a handful of
+# tokens, so their argument checks are kept short: one comparison of type and
+# shape per tensor, addresses passed as plain integers.
+_BF16, _F32 = torch.bfloat16, torch.float32
 
 
-def _rows(recv_rows, *tensors) -> int:
+def _wrong(name, t, dtype, shape):
+    want = "x".join("*" if n is None else str(n) for n in shape)
+    return ValueError(f"{name}: expected {dtype} {want}, got {t.dtype} {tuple(t.shape)}"
+                      + ("" if t.is_contiguous() else ", not contiguous"))
+
+
+def _row_tensor(name, t, width):
+    """Address and rows of a contiguous bf16 [rows][width] tensor."""
+    n, w = t.shape
+    if w != width or t.dtype is not _BF16 or not t.is_contiguous():
+        raise _wrong(name, t, _BF16, (None, width))
+    return t.data_ptr(), n
+
+
+def _tensor(name, t, dtype, shape):
+    """Address of a contiguous tensor of this type and shape."""
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
+        raise _wrong(name, t, dtype, shape)
+    return t.data_ptr()
+
+
+def _raw_stream(stream) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _rows(recv_rows, *held) -> int:
     """Receive rows that every given row tensor holds."""
-    held = min(t.shape[0] for t in tensors if t is not None)
-    return held if recv_rows is None else min(int(recv_rows), held)
-
-
-def _shaped(name, t, *shape) -> None:
-    if t is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+    n = min(held)
+    return n if recv_rows is None else min(int(recv_rows), n)
 
 
 def moe_ep_ffn_gate_up(handle: int, x, w_gate_up, hid, gate_up=None, act: int = MOE_EP_ACT_SILU,
                        recv_rows: int | None = None, stream=None) -> None:
     """x [rows][H], w_gate_up [E][2F][H], hid [rows][F], gate_up [rows][2F] or None."""
-    _typed(torch.bfloat16, x=x, w_gate_up=w_gate_up, hid=hid, gate_up=gate_up)
     E, H = _sizes[handle]
     F = hid.shape[1]
-    _shaped("x", x, x.shape[0], H)
-    _shaped("w_gate_up", w_gate_up, E, 2 * F, H)
-    if gate_up is not None:
-        _shaped("gate_up", gate_up, gate_up.shape[0], 2 * F)
-    _check("moe_ep_ffn_gate_up",
-           _lib.moe_ep_ffn_gate_up(ctypes.c_void_p(handle), _ptr(x), _ptr(w_gate_up), F, act,
-                                   _ptr(hid), _ptr(gate_up), _rows(recv_rows, x, hid, gate_up),
-                                   _stream(stream)))
+    hid_p, n = _row_tensor("hid", hid, F)
+    x_p, nx = _row_tensor("x", x, H)
+    gu_p, ng = (None, n) if gate_up is None else _row_tensor("gate_up", gate_up, 2 * F)
+    st = _lib.moe_ep_ffn_gate_up(handle, x_p, _tensor("w_gate_up", w_gate_up, _BF16, (E, 2 * F, H)),
+                                 F, act, hid_p, gu_p, _rows(recv_rows, n, nx, ng),
+                                 _raw_stream(stream))
+    if st:
+        raise MoeEpError("moe_ep_ffn_gate_up", st)
 
 
 def moe_ep_ffn_down(handle: int, hid, w_down, y, recv_rows: int | None = None, stream=None) -> None:
     """hid [rows][F], w_down [E][H][F], y [rows][H]."""
-    _typed(torch.bfloat16, hid=hid, w_down=w_down, y=y)
     E, H = _sizes[handle]
     F = hid.shape[1]
-    _shaped("y", y, y.shape[0], H)
-    _shaped("w_down", w_down, E, H, F)
-    _check("moe_ep_ffn_down",
-           _lib.moe_ep_ffn_down(ctypes.c_void_p(handle), _ptr(hid), _ptr(w_down), F, _ptr(y),
-                                _rows(recv_rows, hid, y), _stream(stream)))
+    hid_p, n = _row_tensor("hid", hid, F)
+    y_p, ny = _row_tensor("y", y, H)
+    st = _lib.moe_ep_ffn_down(handle, hid_p, _tensor("w_down", w_down, _BF16, (E, H, F)), F, y_p,
+                              _rows(recv_rows, n, ny), _raw_stream(stream))
+    if st:
+        raise MoeEpError("moe_ep_ffn_down", st)
 
 
 def moe_ep_ffn_down_backward(handle: int, dy, w_down, gate_up, d_gate_up, hid=None,
                              act: int = MOE_EP_ACT_SILU, recv_rows: int | None = None,
                              stream=None) -> None:
     """dy [rows][H], w_down [E][H][F], gate_up and d_gate_up [rows][2F], hid [rows][F] or None."""
-    _typed(torch.bfloat16, dy=dy, w_down=w_down, gate_up=gate_up, d_gate_up=d_gate_up, hid=hid)
     E, H = _sizes[handle]
     F = w_down.shape[2]
-    _shaped("dy", dy, dy.shape[0], H)
-    _shaped("w_down", w_down, E, H, F)
-    _shaped("gate_up", gate_up, gate_up.shape[0], 2 * F)
-    _shaped("d_gate_up", d_gate_up, d_gate_up.shape[0], 2 * F)
-    if hid is not None:
-        _shaped("hid", hid, hid.shape[0], F)
-    _check("moe_ep_ffn_down_backward",
-           _lib.moe_ep_ffn_down_backward(ctypes.c_void_p(handle), _ptr(dy), _ptr(w_down),
-                                         _ptr(gate_up), F, act, _ptr(d_gate_up), _ptr(hid),
-                                         _rows(recv_rows, dy, gate_up, d_gate_up, hid),
-                                         _stream(stream)))
+    dy_p, n = _row_tensor("dy", dy, H)
+    gu_p, ng = _row_tensor("gate_up", gate_up, 2 * F)
+    dgu_p, nd = _row_tensor("d_gate_up", d_gate_up, 2 * F)
+    hid_p, nh = (None, n) if hid is None else _row_tensor("hid", hid, F)
+    st = _lib.moe_ep_ffn_down_backward(handle, dy_p, _tensor("w_down", w_down, _BF16, (E, H, F)),
+                                       gu_p, F, act, dgu_p, hid_p, _rows(recv_rows, n, ng, nd, nh),
+                                       _raw_stream(stream))
+    if st:
+        raise MoeEpError("moe_ep_ffn_down_backward", st)
 
 
 def moe_ep_ffn_gate_up_backward(handle: int, d_gate_up, w_gate_up, dx,
                                 recv_rows: int | None = None, stream=None) -> None:
     """d_gate_up [rows][2F], w_gate_up [E][2F][H], dx [rows][H]."""
-    _typed(torch.bfloat16, d_gate_up=d_gate_up, w_gate_up=w_gate_up, dx=dx)
     E, H = _sizes[handle]
     F2 = d_gate_up.shape[1]
-    _shaped("dx", dx, dx.shape[0], H)
-    _shaped("w_gate_up", w_gate_up, E, F2, H)
     if F2 % 2:
         raise ValueError("d_gate_up: gate and up columns expected")
-    _check("moe_ep_ffn_gate_up_backward",
-           _lib.moe_ep_ffn_gate_up_backward(ctypes.c_void_p(handle), _ptr(d_gate_up),
-                                            _ptr(w_gate_up), F2 // 2, _ptr(dx),
-                                            _rows(recv_rows, d_gate_up, dx), _stream(stream)))
+    dgu_p, n = _row_tensor("d_gate_up", d_gate_up, F2)
+    dx_p, nx = _row_tensor("dx", dx, H)
+    st = _lib.moe_ep_ffn_gate_up_backward(handle, dgu_p,
+                                          _tensor("w_gate_up", w_gate_up, _BF16, (E, F2, H)),
+                                          F2 // 2, dx_p, _rows(recv_rows, n, nx),
+                                          _raw_stream(stream))
+    if st:
+        raise MoeEpError("moe_ep_ffn_gate_up_backward", st)
 
 
 def moe_ep_ffn_weight_grad(handle: int, a, b, dw, accumulate: bool = False,
                            recv_rows: int | None = None, stream=None) -> None:
     """a [rows][m], b [rows][n] bf16, dw [E][m][n] bf16 or fp32."""
-    _typed(torch.bfloat16, a=a, b=b)
-    if dw.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"dw: expected bf16 or fp32, got {dw.dtype}")
-    _shaped("dw", dw, _sizes[handle][0], a.shape[1], b.shape[1])
-    _check("moe_ep_ffn_weight_grad",
-           _lib.moe_ep_ffn_weight_grad(ctypes.c_void_p(handle), _ptr(a), a.shape[1], _ptr(b),
-                                       b.shape[1], _ptr(dw), int(dw.dtype == torch.float32),
-                                       int(bool(accumulate)), _rows(recv_rows, a, b),
-                                       _stream(stream)))
+    m, n = a.shape[1], b.shape[1]
+    a_p, na = _row_tensor("a", a, m)
+    b_p, nb = _row_tensor("b", b, n)
+    f32 = dw.dtype is _F32
+    dw_p = _tensor("dw", dw, _F32 if f32 else _BF16, (_sizes[handle][0], m, n))
+    st = _lib.moe_ep_ffn_weight_grad(handle, a_p, m, b_p, n, dw_p, int(f32), int(bool(accumulate)),
+                                     _rows(recv_rows, na, nb), _raw_stream(stream))
+    if st:
+        raise MoeEpError("moe_ep_ffn_weight_grad", st)
 
 
 def moe_ep_combine_backward(handle: int, dout, y, topk_w, dy, dw, recv_rows: int | None = None,
                             stream=None) -> None:
     """dout [T][H], y and dy [rows][H] bf16, topk_w and dw [T][k] fp32."""
-    _typed(torch.bfloat16, dout=dout, y=y, dy=dy)
-    _typed(torch.float32, topk_w=topk_w, dw=dw)
     H = _sizes[handle][1]
-    for name, t in (("dout", dout), ("y", y), ("dy", dy)):
-        _shaped(name, t, t.shape[0], H)
-    _shaped("dw", dw, *topk_w.shape)
-    _check("moe_ep_combine_backward",
-           _lib.moe_ep_combine_backward(ctypes.c_void_p(handle), _ptr(dout), _ptr(y), _ptr(topk_w),
-                                        _ptr(dy), _ptr(dw), _rows(recv_rows, y, dy),
-                                        _stream(stream)))
+    y_p, n = _row_tensor("y", y, H)
+    dy_p, nd = _row_tensor("dy", dy, H)
+    pairs = topk_w.shape
+    st = _lib.moe_ep_combine_backward(handle, _row_tensor("dout", dout, H)[0], y_p,
+                                      _tensor("topk_w", topk_w, _F32, pairs), dy_p,
+                                      _tensor("dw", dw, _F32, pairs), _rows(recv_rows, n, nd),
+                                      _raw_stream(stream))
+    if st:
+        raise MoeEpError("moe_ep_combine_backward", st)
 
 
-def _norm_sizes(group, num_tokens, per_token, tokens: dict, channels: dict, gates: dict) -> int:
-    """The number of tokens, after checking every given tensor's shape against it and H."""
-    H = _sizes[group][1]
-    T = num_tokens
-    if T is None:
-        T = next((t.shape[0] for t in tokens.values() if t is not None), 0)
-    for name, t in tokens.items():
-        if t is not None and (t.dim() != 2 or t.shape[0] < T or t.shape[1] != H):
-            raise ValueError(f"{name}: expected [{T}][{H}], got {tuple(t.shape)}")
-    for name, t in channels.items():
-        _shaped(name, t, H)
-    for name, t in gates.items():
-        if t is not None and t.numel() < (T if per_token else H):
-            raise ValueError(f"{name}: expected {T if per_token else H} values, got {t.numel()}")
-    return T
+def _token_tensor(name, t, T, H):
+    """Address of a contiguous bf16 tensor with at least T rows of H, or None."""
+    if t is None:
+        return None
+    p, n = _row_tensor(name, t, H)
+    if n < T:
+        raise _wrong(name, t, _BF16, (T, H))
+    return p
+
+
+def _channels(name, t, n):
+    """Address of at least n contiguous fp32 values, or None."""
+    if t is None:
+        return None
+    if t.dtype is not _F32 or t.numel() < n or not t.is_contiguous():
+        raise _wrong(name, t, _F32, (n,))
+    return t.data_ptr()
 
 
 def moe_ep_norm_residual(group: int, o, res, w_post, gate, w_pre, res_out, y,
                          res_scale: float = 1.0, gate_per_token: bool = False, eps: float = 1e-6,
                          num_tokens: int | None = None, stream=None) -> None:
     """o, res, res_out, y [T][H] bf16, w_post, w_pre [H] and gate [H] or [T] fp32; None for absent."""
-    _typed(torch.bfloat16, o=o, res=res, res_out=res_out, y=y)
-    _typed(torch.float32, w_post=w_post, gate=gate, w_pre=w_pre)
-    T = _norm_sizes(group, num_tokens, gate_per_token, dict(o=o, res=res, res_out=res_out, y=y),
-                    dict(w_post=w_post, w_pre=w_pre), dict(gate=gate))
-    _check("moe_ep_norm_residual",
-           _lib.moe_ep_norm_residual(ctypes.c_void_p(group), _ptr(o), _ptr(res), _ptr(w_post),
-                                     _ptr(gate), int(bool(gate_per_token)), _ptr(w_pre), res_scale,
-                                     eps, T, _ptr(res_out), _ptr(y), _stream(stream)))
+    H = _sizes[group][1]
+    first = res if o is None else o
+    T = num_tokens if num_tokens is not None else 0 if first is None else first.shape[0]
+    st = _lib.moe_ep_norm_residual(group, _token_tensor("o", o, T, H),
+                                   _token_tensor("res", res, T, H), _channels("w_post", w_post, H),
+                                   _channels("gate", gate, T if gate_per_token else H),
+                                   1 if gate_per_token else 0, _channels("w_pre", w_pre, H),
+                                   res_scale, eps, T, _token_tensor("res_out", res_out, T, H),
+                                   _token_tensor("y", y, T, H), _raw_stream(stream))
+    if st:
+        raise MoeEpError("moe_ep_norm_residual", st)
 
 
 def moe_ep_norm_work_floats(group: int) -> int:
@@ -458,21 +481,20 @@ def moe_ep_norm_residual_backward(group: int, o, res, w_post, gate, w_pre, dr, d
                                   num_tokens: int | None = None, stream=None) -> None:
     """dr, dy, d_o, dres [T][H] bf16, dw_post, dw_pre [H] and dgate (as gate) fp32, work
     [moe_ep_norm_work_floats] fp32; None for absent."""
-    _typed(torch.bfloat16, o=o, res=res, dr=dr, dy=dy, d_o=d_o, dres=dres)
-    _typed(torch.float32, w_post=w_post, gate=gate, w_pre=w_pre, dw_post=dw_post, dgate=dgate,
-           dw_pre=dw_pre, work=work)
-    T = _norm_sizes(group, num_tokens, gate_per_token,
-                    dict(o=o, res=res, dr=dr, dy=dy, d_o=d_o, dres=dres),
-                    dict(w_post=w_post, w_pre=w_pre, dw_post=dw_post, dw_pre=dw_pre),
-                    dict(gate=gate, dgate=dgate))
-    if work is not None and work.numel() < moe_ep_norm_work_floats(group):
-        raise ValueError("work: too small (moe_ep_norm_work_floats)")
-    _check("moe_ep_norm_residual_backward",
-           _lib.moe_ep_norm_residual_backward(ctypes.c_void_p(group), _ptr(o), _ptr(res),
-                                              _ptr(w_post), _ptr(gate), int(bool(gate_per_token)),
-                                              _ptr(w_pre), res_scale, eps, T, _ptr(dr), _ptr(dy),
-                                              _ptr(d_o), _ptr(dres), _ptr(dw_post), _ptr(dgate),
-                                              _ptr(dw_pre), _ptr(work), _stream(stream)))
+    H = _sizes[group][1]
+    first = res if o is None else o
+    T = num_tokens if num_tokens is not None else 0 if first is None else first.shape[0]
+    gates = T if gate_per_token else H
+    st = _lib.moe_ep_norm_residual_backward(
+        group, _token_tensor("o", o, T, H), _token_tensor("res", res, T, H),
+        _channels("w_post", w_post, H), _channels("gate", gate, gates), 1 if gate_per_token else 0,
+        _channels("w_pre", w_pre, H), res_scale, eps, T, _token_tensor("dr", dr, T, H),
+        _token_tensor("dy", dy, T, H), _token_tensor("d_o", d_o, T, H),
+        _token_tensor("dres", dres, T, H), _channels("dw_post", dw_post, H),
+        _channels("dgate", dgate, gates), _channels("dw_pre", dw_pre, H),
+        _channels("work", work, moe_ep_norm_work_floats(group)), _raw_stream(stream))
+    if st:
+        raise MoeEpError("moe_ep_norm_residual_backward", st)
 
 
 def moe_ep_get_device_errors(group: int) -> int:
