@@ -2,17 +2,19 @@
 // on the fifth-generation tensor cores: products of the rows with their
 // expert's weights, the activation fused into the product that feeds it.
 //
-// Orientation.  A tile is 128 weight rows (features) x up to 256 receive rows
-// of one expert: the weights are the tensor core's 128-row operand and the
-// tokens its n dimension, which any multiple of 16 up to 256 serves.  An
+// Orientation.  A tile is 256 weight rows (features) x up to 256 receive rows
+// of one expert, shared by a pair of CTAs (cta_group::2): the weights are the
+// tensor core's fixed operand of 2 x 128 rows and the tokens its n dimension,
+// which any multiple of 32 up to 256 serves.  An
 // expert's share of a batch is ragged and often small (a decoding step gives
 // an expert a handful of rows), so the ragged dimension goes where the
 // instruction takes it; with tokens on the 128-row side an expert with 5 rows
-// would cost as much as one with 128.
+// would cost as much as one with 128.  The pair halves what a CTA stages of the tokens: 32 KB for
+// 128 x 256 x 64 products per CTA where a CTA alone stages 48 KB.
 //
-// Roles of a CTA (192 threads): one thread loads operand tiles by TMA into a
-// ring of shared-memory stages, one thread issues the products, four warps
-// read the fp32 accumulators from tensor memory, apply the activation and
+// Roles of a CTA (192 threads): one thread loads its operand tiles by TMA into a
+// ring of shared-memory stages, one thread of the pair's first CTA issues the
+// products, four warps read the fp32 accumulators from tensor memory, apply the activation and
 // store bf16.  The accumulators are double-buffered, so a tile's epilogue runs
 // under the next tile's products.  CTAs are persistent; the tile list is
 // derived on the device from the layout's counts (no host synchronisation).
@@ -27,13 +29,15 @@ namespace {
 
 constexpr int kThreads = 192;
 constexpr int kKB = 64;      // contraction elements per stage (128 bytes of bf16)
-constexpr int kTileM = 128;  // weight rows per tile
+constexpr int kTileM = 128;  // weight rows per CTA, 256 per pair
+constexpr int kTileN = 256;  // receive rows per tile, at most
+constexpr int kStages = 6;
 constexpr int kBand = 8;     // n tiles that share the weights of one pass over an expert
 
 // Shared-memory control block of a CTA.
 template <int STAGES>
 struct Control {
-    uint64_t full[STAGES], empty[STAGES];
+    uint64_t full[STAGES], empty[STAGES], ready[STAGES];
     uint64_t acc_full[2], acc_empty[2];
     uint64_t drain;
     uint32_t tmem;
@@ -42,6 +46,15 @@ struct Control {
     int cnt[kMaxExperts];
     int pre[kMaxExperts + 1];  // n tiles before each expert
 };
+
+// One whole 32-byte sector.
+__device__ __forceinline__ void store32(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e,
+                                        uint32_t f, uint32_t g, uint32_t h)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a), "r"(b), "r"(c),
+                 "r"(d), "r"(e), "r"(f), "r"(g), "r"(h)
+                 : "memory");
+}
 
 __device__ __forceinline__ void give_up(volatile int* dead, unsigned* err)
 {
@@ -89,7 +102,7 @@ struct Tile {
     int m;         // m tile
     int row;       // first receive row
     int rows;      // valid rows
-    int n;         // rows of the product (a multiple of 16)
+    int n;         // rows of the product (a multiple of 32)
 
     __device__ __forceinline__ void find(int i, const int* cnt, const int* pre, int mt, const RowsArgs& a)
     {
@@ -102,9 +115,9 @@ struct Tile {
         m = q / nb;
         const int j = b * kBand + (q - m * nb);
         // equal tiles, in steps of the instruction's n granularity
-        const int w = ((c + nt - 1) / nt + 15) & ~15;
+        const int w = ((c + nt - 1) / nt + 31) & ~31;
         rows = min(w, c - j * w);
-        n = (rows + 15) & ~15;
+        n = (rows + 31) & ~31;
         row = (a.mode == MOE_EP_HT ? __ldg(a.off + e) : e * a.S) + j * w;
     }
 };
@@ -188,38 +201,79 @@ __device__ __forceinline__ void epi_down_bwd(const float (&v)[16], const RowsArg
         }
 }
 
-template <int EPI, int NT, int STAGES>
-__global__ void __launch_bounds__(kThreads, 1)
-    rows_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ RowMaps rmap,
-                const RowsArgs a)
+// Barriers, tensor memory and the pair; every thread of both CTAs.
+template <int STAGES>
+__device__ __forceinline__ void start_pair(Control<STAGES>& c, int warp)
 {
-    constexpr bool A_MN = EPI == kRowsDownBwd || EPI == kRowsStoreT;
-    constexpr int kABytes = kTileM * kKB * 2, kStageBytes = kABytes + NT * kKB * 2;
-    extern __shared__ uint8_t dyn[];
-    __shared__ Control<STAGES> c;
-    const int warp = threadIdx.x >> 5;
-    const uint32_t ring = (smem_u32(dyn) + 1023u) & ~1023u;
-
     if (threadIdx.x == 0) {
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(smem_u32(&c.full[i]), 1);
             mbar_init(smem_u32(&c.empty[i]), 1);
+            mbar_init(smem_u32(&c.ready[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&c.acc_full[i]), 1);
-            mbar_init(smem_u32(&c.acc_empty[i]), 4);
+            mbar_init(smem_u32(&c.acc_empty[i]), 8);  // the epilogue warps of both CTAs
         }
         mbar_init(smem_u32(&c.drain), 1);
         c.dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        tma_prefetch_map(&wmap);
     }
-    if (warp == 1) tmem_alloc(smem_u32(&c.tmem), 2 * NT);
-    griddep_wait();
+    if (warp == 1) tmem_alloc(smem_u32(&c.tmem), 512);
     tc_fence_before();
-    tile_prefix(a.cnt, a.E, NT, c.cnt, c.pre, c.part);  // barriers inside: also publishes the above
+    cluster_sync();
     tc_fence_after();
-    const int total = c.pre[a.E] * a.mt;
+}
+
+// Nothing may still arrive at a CTA that has left: both leave together.
+template <int STAGES>
+__device__ __forceinline__ void end_pair(Control<STAGES>& c, int warp)
+{
+    __syncwarp();
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    if (warp == 1) tmem_free(c.tmem, 512);
+}
+
+// A producer that gave up waits (with a limit) for the copies in flight: they
+// land in the pair's shared memory.
+template <int STAGES>
+__device__ __forceinline__ void drain_copies(Control<STAGES>& c, uint32_t issued, unsigned* err)
+{
+    give_up(&c.dead, err);
+    volatile int go_on = 0;
+    for (uint32_t j = issued < STAGES ? 0 : issued - STAGES; j < issued; ++j)
+        mbar_wait(smem_u32(&c.full[j % STAGES]), (j / STAGES) & 1u, &go_on);
+}
+// ... and an issuer for its products, which read that memory.
+template <int STAGES>
+__device__ __forceinline__ void drain_products(Control<STAGES>& c, unsigned* err)
+{
+    give_up(&c.dead, err);
+    volatile int go_on = 0;
+    tc_commit(smem_u32(&c.drain));
+    mbar_wait(smem_u32(&c.drain), 0, &go_on);
+}
+
+template <int EPI>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    rows_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ RowMaps rmap,
+                const RowsArgs a)
+{
+    constexpr bool A_MN = EPI == kRowsDownBwd || EPI == kRowsStoreT;
+    constexpr int STAGES = kStages;
+    constexpr int kABytes = kTileM * kKB * 2, kStageBytes = kABytes + kTileN / 2 * kKB * 2;
+    extern __shared__ uint8_t dyn[];
+    __shared__ Control<STAGES> c;
+    const int warp = threadIdx.x >> 5;
+    const uint32_t rank = cluster_rank();
+    const uint32_t ring = (smem_u32(dyn) + 1023u) & ~1023u;
+
+    start_pair(c, warp);
+    griddep_wait();
+    tile_prefix(a.cnt, a.E, kTileN, c.cnt, c.pre, c.part);
+    const int total = c.pre[a.E] * a.mt, first = blockIdx.x >> 1, step = gridDim.x >> 1;
     const int kblocks = (a.K + kKB - 1) / kKB;
 
     if (warp == 0) {
@@ -227,47 +281,43 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t it = 0;  // k blocks loaded
             Tile t;
             bool ok = true;
-            for (int i = blockIdx.x; i < total && ok; i += gridDim.x) {
+            for (int i = first; i < total && ok; i += step) {
                 t.find(i, c.cnt, c.pre, a.mt, a);
+                const int m = t.m * 2 + (int)rank, half = t.n / 2, row = t.row + (int)rank * half;
                 for (int kb = 0; kb < kblocks; ++kb, ++it) {
                     const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
                     if (!mbar_wait(smem_u32(&c.empty[s]), ph ^ 1u, &c.dead)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t bar = smem_u32(&c.full[s]);
+                    // both CTAs' bytes are counted on the first one's barrier
+                    const uint32_t bar = in_cta(smem_u32(&c.full[s]), 0);
                     const uint32_t sa = ring + s * kStageBytes, sb = sa + kABytes;
-                    mbar_expect_tx(bar, kABytes + t.n * kKB * 2);
+                    if (rank == 0) mbar_expect_tx(smem_u32(&c.full[s]), 2 * kABytes + t.n * kKB * 2);
                     const int k0 = kb * kKB;
                     if (EPI == kRowsGateUp) {
                         // [expert][f / 8][gate, up][f % 8][H]: 8 gate and 8 up rows in turn
-                        tma_load(sa, &wmap, bar, k0, 0, 0, t.m * (kTileM / 16), t.e);
+                        tma_load(sa, &wmap, bar, k0, 0, 0, m * (kTileM / 16), t.e);
                     } else if (A_MN) {
-                        tma_load(sa, &wmap, bar, t.m * kTileM, k0, t.e);
-                        tma_load(sa + kABytes / 2, &wmap, bar, t.m * kTileM + 64, k0, t.e);
+                        tma_load(sa, &wmap, bar, m * kTileM, k0, t.e);
+                        tma_load(sa + kABytes / 2, &wmap, bar, m * kTileM + 64, k0, t.e);
                     } else {
-                        tma_load(sa, &wmap, bar, k0, t.m * kTileM, t.e);
+                        tma_load(sa, &wmap, bar, k0, m * kTileM, t.e);
                     }
                     for (int b = 0, r = 0; b < kRowBoxes; ++b) {
                         const int h = 128 >> b;
-                        for (; t.n - r >= h; r += h) tma_load(sb + r * 128, &rmap.box[b], bar, k0, t.row + r);
+                        for (; half - r >= h; r += h) tma_load(sb + r * 128, &rmap.box[b], bar, k0, row + r);
                     }
                 }
             }
-            if (!ok) {
-                give_up(&c.dead, a.err);
-                // the copies still in flight land in this CTA's shared memory
-                volatile int go_on = 0;
-                for (uint32_t j = it < STAGES ? 0 : it - STAGES; j < it; ++j)
-                    mbar_wait(smem_u32(&c.full[j % STAGES]), (j / STAGES) & 1u, &go_on);
-            }
+            if (!ok) drain_copies(c, rank == 0 ? it : 0, a.err);
         }
     } else if (warp == 1) {
-        if (elect_one()) {
+        if (rank == 0 && elect_one()) {
             uint32_t it = 0, tile = 0;
             Tile t;
             bool ok = true;
-            for (int i = blockIdx.x; i < total && ok; i += gridDim.x, ++tile) {
+            for (int i = first; i < total && ok; i += step, ++tile) {
                 t.find(i, c.cnt, c.pre, a.mt, a);
                 const uint32_t acc = tile & 1u;
                 if (!mbar_wait(smem_u32(&c.acc_empty[acc]), ((tile >> 1) & 1u) ^ 1u, &c.dead)) {
@@ -275,8 +325,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 tc_fence_after();
-                const uint32_t d = c.tmem + acc * NT;
-                const uint32_t idesc = tc_idesc(kTileM, t.n, A_MN, 0);
+                const uint32_t d = c.tmem + acc * kTileN;
+                const uint32_t idesc = tc_idesc(2 * kTileM, t.n, A_MN, 0);
                 for (int kb = 0; kb < kblocks; ++kb, ++it) {
                     const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
                     if (!mbar_wait(smem_u32(&c.full[s]), ph, &c.dead)) {
@@ -294,18 +344,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (ok) tc_commit(smem_u32(&c.acc_full[acc]));
             }
-            if (!ok) {
-                give_up(&c.dead, a.err);
-                volatile int go_on = 0;
-                tc_commit(smem_u32(&c.drain));
-                mbar_wait(smem_u32(&c.drain), 0, &go_on);
-            }
+            if (!ok) drain_products(c, a.err);
         }
     } else {
         const int lane = threadIdx.x & 31, quarter = warp & 3;  // tensor-memory lanes of this warp
         uint32_t tile = 0;
         Tile t;
-        for (int i = blockIdx.x; i < total; i += gridDim.x, ++tile) {
+        for (int i = first; i < total; i += step, ++tile) {
             t.find(i, c.cnt, c.pre, a.mt, a);
             const uint32_t acc = tile & 1u;
             if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&c.acc_full[acc]), (tile >> 1) & 1u, &c.dead))) {
@@ -313,8 +358,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             }
             tc_fence_after();
-            const uint32_t src = c.tmem + acc * NT + ((uint32_t)(quarter * 32) << 16);
-            const int r = t.m * kTileM + quarter * 32 + lane;  // tile row
+            const uint32_t src = c.tmem + acc * kTileN + ((uint32_t)(quarter * 32) << 16);
+            const int r = (t.m * 2 + (int)rank) * kTileM + quarter * 32 + lane;  // weight row
             for (int c0 = 0; c0 < t.n; c0 += 16) {
                 float v[16];
                 tmem_ld16(src + c0, v);
@@ -329,68 +374,93 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&c.acc_empty[acc]));
+            if (lane == 0) mbar_arrive_cluster(in_cta(smem_u32(&c.acc_empty[acc]), 0));
         }
     }
-    __syncwarp();
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    if (warp == 1) tmem_free(c.tmem, 2 * NT);
+    end_pair(c, warp);
 }
 
 // ---------------------------------------------------------------------------
 // Weight gradients: dW[e] = sum over the expert's rows of a_row b_row^T.  Both
 // operands are read with their features contiguous (rows are the contraction);
-// a tile is 128 x 256 of one expert's gradient.  The last block of an
-// expert's rows may reach into rows that are not its own (the next expert's,
-// or slots that were never written): the issuing warp clears those rows of
-// both operands in shared memory before the product, because 0 x NaN would
-// not be 0.
-constexpr int kGradN = 256, kGradStages = 4;
+// a tile is 256 x 256 of one expert's gradient, 128 x 256 in each CTA.  The last
+// block of an expert's rows may reach into rows that are not its own (the next
+// expert's, or slots that were never written): those rows of both operands are
+// cleared in shared memory before the product, because 0 x NaN would not be 0.
+// For that each CTA's copies are counted on its own barrier; the second CTA's
+// issuing warp clears its rows and passes the block on to the first one's
+// (`ready`), which clears its own and issues.
+template <bool F32>
+__device__ __forceinline__ void store_grad(const float (&v)[16], const GradArgs& a, size_t at, int n, bool wide)
+{
+    if (F32) {
+        float* p = (float*)a.dw + at;
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = v[i];
+        if (a.accumulate) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+                if (i < n) {
+                    const float4 o = *reinterpret_cast<const float4*>(p + i);
+                    x[i] += o.x; x[i + 1] += o.y; x[i + 2] += o.z; x[i + 3] += o.w;
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < 16; i += 8)
+            if (i < n) {
+                if (wide) {
+                    store32(p + i, __float_as_uint(x[i]), __float_as_uint(x[i + 1]), __float_as_uint(x[i + 2]),
+                            __float_as_uint(x[i + 3]), __float_as_uint(x[i + 4]), __float_as_uint(x[i + 5]),
+                            __float_as_uint(x[i + 6]), __float_as_uint(x[i + 7]));
+                } else {
+                    *reinterpret_cast<float4*>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                    *reinterpret_cast<float4*>(p + i + 4) = make_float4(x[i + 4], x[i + 5], x[i + 6], x[i + 7]);
+                }
+            }
+    } else {
+        __nv_bfloat16* p = (__nv_bfloat16*)a.dw + at;
+        uint32_t o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            o[i] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        if (wide && n >= 16) {
+            store32(p, o[0], o[1], o[2], o[3], o[4], o[5], o[6], o[7]);
+        } else {
+            *reinterpret_cast<uint4*>(p) = make_uint4(o[0], o[1], o[2], o[3]);
+            if (n >= 16) *reinterpret_cast<uint4*>(p + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+    }
+}
 
 template <bool F32>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     grad_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
                 const GradArgs a)
 {
-    constexpr int kABytes = kTileM * kKB * 2, kStageBytes = kABytes + kGradN * kKB * 2;
+    constexpr int STAGES = kStages;
+    constexpr int kABytes = kTileM * kKB * 2, kStageBytes = 2 * kABytes;
     constexpr int kBlock = 64 * kKB * 2;  // 64 features x 64 rows
-    constexpr int STAGES = kGradStages;
     extern __shared__ uint8_t dyn[];
     __shared__ Control<STAGES> c;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
     const uint32_t ring = (smem_u32(dyn) + 1023u) & ~1023u;
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < STAGES; ++i) {
-            mbar_init(smem_u32(&c.full[i]), 1);
-            mbar_init(smem_u32(&c.empty[i]), 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&c.acc_full[i]), 1);
-            mbar_init(smem_u32(&c.acc_empty[i]), 4);
-        }
-        mbar_init(smem_u32(&c.drain), 1);
-        c.dead = 0;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        tma_prefetch_map(&amap);
-        tma_prefetch_map(&bmap);
-    }
-    if (warp == 1) tmem_alloc(smem_u32(&c.tmem), 2 * kGradN);
+    start_pair(c, warp);
     griddep_wait();
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
     const int per = a.mt * a.nt;
-    const int64_t total = (int64_t)per * a.E;
+    const int64_t total = (int64_t)per * a.E, first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
     if (warp == 0) {
         if (elect_one()) {
             uint32_t it = 0;
             bool ok = true;
-            for (int64_t i = blockIdx.x; i < total && ok; i += gridDim.x) {
+            for (int64_t i = first; i < total && ok; i += step) {
                 const int e = (int)(i / per), q = (int)(i - (int64_t)e * per);
-                const int m0 = (q / a.nt) * kTileM, n0 = (q % a.nt) * kGradN;
+                const int m0 = ((q / a.nt) * 2 + (int)rank) * kTileM;
+                const int n0 = (q % a.nt) * kTileN + (int)rank * (kTileN / 2);
                 const int rows = __ldg(a.cnt + e), base = a.mode == MOE_EP_HT ? __ldg(a.off + e) : e * a.S;
                 for (int r = 0; r < rows; r += kKB, ++it) {
                     const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
@@ -401,30 +471,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t bar = smem_u32(&c.full[s]);
                     const uint32_t sa = ring + s * kStageBytes, sb = sa + kABytes;
                     mbar_expect_tx(bar, kStageBytes);
-                    for (int b = 0; b < kTileM / 64; ++b) tma_load(sa + b * kBlock, &amap, bar, m0 + b * 64, base + r);
-                    for (int b = 0; b < kGradN / 64; ++b) tma_load(sb + b * kBlock, &bmap, bar, n0 + b * 64, base + r);
+                    for (int b = 0; b < 2; ++b) {
+                        tma_load(sa + b * kBlock, &amap, bar, m0 + b * 64, base + r);
+                        tma_load(sb + b * kBlock, &bmap, bar, n0 + b * 64, base + r);
+                    }
                 }
             }
-            if (!ok) {
-                give_up(&c.dead, a.err);
-                volatile int go_on = 0;
-                for (uint32_t j = it < STAGES ? 0 : it - STAGES; j < it; ++j)
-                    mbar_wait(smem_u32(&c.full[j % STAGES]), (j / STAGES) & 1u, &go_on);
-            }
+            if (!ok) drain_copies(c, it, a.err);
         }
     } else if (warp == 1) {
         uint32_t it = 0, tile = 0;
         bool ok = true;
-        const uint32_t idesc = tc_idesc(kTileM, kGradN, 1, 1);
-        for (int64_t i = blockIdx.x; i < total && ok; i += gridDim.x) {
-            const int e = (int)(i / per);
-            const int rows = __ldg(a.cnt + e);
+        const uint32_t idesc = tc_idesc(2 * kTileM, kTileN, 1, 1);
+        for (int64_t i = first; i < total && ok; i += step) {
+            const int rows = __ldg(a.cnt + (int)(i / per));
             if (rows == 0) continue;
             const uint32_t acc = tile & 1u;
-            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&c.acc_empty[acc]), ((tile >> 1) & 1u) ^ 1u, &c.dead));
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t d = c.tmem + acc * kGradN;
+            if (rank == 0) {
+                ok = __all_sync(0xffffffffu,
+                                mbar_wait(smem_u32(&c.acc_empty[acc]), ((tile >> 1) & 1u) ^ 1u, &c.dead));
+                if (!ok) break;
+                tc_fence_after();
+            }
+            const uint32_t d = c.tmem + acc * kTileN;
             for (int r = 0; r < rows; r += kKB, ++it) {
                 const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
                 ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&c.full[s]), ph, &c.dead));
@@ -435,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // rows left .. steps * 16 of every 64-feature block (the
                     // swizzle moves 16-byte units within a row's 128 bytes only)
                     const int units = (steps * 16 - left) * 8;
-                    for (int b = 0; b < (kTileM + kGradN) / 64; ++b)
+                    for (int b = 0; b < kStageBytes / kBlock; ++b)
                         for (int x = lane; x < units; x += 32)
                             asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
                                              sa + b * kBlock + left * 128 + x * 16),
@@ -444,6 +513,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                 }
+                if (rank != 0) {
+                    if (lane == 0) mbar_arrive_cluster(in_cta(smem_u32(&c.ready[s]), 0));
+                    continue;
+                }
+                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&c.ready[s]), ph, &c.dead));
+                if (!ok) break;
                 tc_fence_after();
                 if (lane == 0) {
                     for (int k = 0; k < steps; ++k)
@@ -453,24 +528,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
             }
-            if (ok && lane == 0) tc_commit(smem_u32(&c.acc_full[acc]));
+            if (ok && rank == 0 && lane == 0) tc_commit(smem_u32(&c.acc_full[acc]));
             __syncwarp();
             ++tile;
         }
         if (!ok && lane == 0) {
-            give_up(&c.dead, a.err);
-            volatile int go_on = 0;
-            tc_commit(smem_u32(&c.drain));
-            mbar_wait(smem_u32(&c.drain), 0, &go_on);
+            if (rank == 0)
+                drain_products(c, a.err);
+            else
+                give_up(&c.dead, a.err);
         }
     } else {
         const int quarter = warp & 3;
+        // 32-byte stores need rows that start on 32 bytes
+        const bool wide = a.N % 16 == 0 && ((uintptr_t)a.dw & 31u) == 0;
         uint32_t tile = 0;
-        for (int64_t i = blockIdx.x; i < total; i += gridDim.x) {
+        for (int64_t i = first; i < total; i += step) {
             const int e = (int)(i / per), q = (int)(i - (int64_t)e * per);
-            const int m = (q / a.nt) * kTileM + quarter * 32 + lane, n0 = (q % a.nt) * kGradN;
-            const int rows = __ldg(a.cnt + e);
-            const bool some = rows > 0;
+            const int m = ((q / a.nt) * 2 + (int)rank) * kTileM + quarter * 32 + lane, n0 = (q % a.nt) * kTileN;
+            const bool some = __ldg(a.cnt + e) > 0;
             if (!some && a.accumulate) continue;
             const uint32_t acc = tile & 1u;
             if (some) {
@@ -481,9 +557,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc_fence_after();
             }
-            const uint32_t src = c.tmem + acc * kGradN + ((uint32_t)(quarter * 32) << 16);
+            const uint32_t src = c.tmem + acc * kTileN + ((uint32_t)(quarter * 32) << 16);
             const size_t at = ((size_t)e * a.M + m) * a.N + n0;
-            for (int c0 = 0; c0 < kGradN; c0 += 16) {
+            const int cols = min(kTileN, a.N - n0);
+            for (int c0 = 0; c0 < cols; c0 += 16) {
                 float v[16];
                 if (some) {
                     tmem_ld16(src + c0, v);
@@ -491,56 +568,29 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 16; ++j) v[j] = 0.f;
                 }
-                if (m >= a.M) continue;
-#pragma unroll
-                for (int h = 0; h < 16; h += 8) {
-                    if (n0 + c0 + h >= a.N) break;
-                    if (F32) {
-                        float4* p = reinterpret_cast<float4*>((float*)a.dw + at + c0 + h);
-#pragma unroll
-                        for (int w = 0; w < 2; ++w) {
-                            float4 x = make_float4(v[h + 4 * w], v[h + 4 * w + 1], v[h + 4 * w + 2], v[h + 4 * w + 3]);
-                            if (a.accumulate) {
-                                const float4 o = p[w];
-                                x = make_float4(x.x + o.x, x.y + o.y, x.z + o.z, x.w + o.w);
-                            }
-                            p[w] = x;
-                        }
-                    } else {
-                        uint32_t o[4];
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            const __nv_bfloat162 b = __floats2bfloat162_rn(v[h + 2 * w], v[h + 2 * w + 1]);
-                            o[w] = *reinterpret_cast<const uint32_t*>(&b);
-                        }
-                        *reinterpret_cast<uint4*>((__nv_bfloat16*)a.dw + at + c0 + h) =
-                            make_uint4(o[0], o[1], o[2], o[3]);
-                    }
-                }
+                if (m < a.M) store_grad<F32>(v, a, at + c0, cols - c0, wide);
             }
             if (some) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&c.acc_empty[acc]));
+                if (lane == 0) mbar_arrive_cluster(in_cta(smem_u32(&c.acc_empty[acc]), 0));
                 ++tile;
             }
         }
     }
-    __syncwarp();
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    if (warp == 1) tmem_free(c.tmem, 2 * kGradN);
+    end_pair(c, warp);
 }
 
-template <int EPI, int NT, int STAGES>
-cudaError_t launch_rows(const CUtensorMap& w, const RowMaps& r, const RowsArgs& a, int grid, cudaStream_t s)
+constexpr int kSmem = kStages * 2 * kTileM * kKB * 2 + 1024;
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pairs(void (*k)(KArgs...), int64_t pairs, int sm_count, cudaStream_t s, const Args&... args)
 {
-    constexpr int smem = STAGES * (kTileM + NT) * kKB * 2 + 1024;
-    cudaError_t e = cudaFuncSetAttribute(rows_kernel<EPI, NT, STAGES>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    return launch_pdl_smem(rows_kernel<EPI, NT, STAGES>, dim3(grid), dim3(kThreads), smem, s, w, r, a);
+    const int most = sm_count / 2;
+    const int n = (int)(pairs < most ? pairs : most);
+    return launch_pdl_smem(k, dim3(2 * n), dim3(kThreads), kSmem, s, args...);
 }
 
 }  // namespace
@@ -548,7 +598,6 @@ cudaError_t launch_rows(const CUtensorMap& w, const RowMaps& r, const RowsArgs& 
 cudaError_t launch_rows_product(int epi, const void* rows_in, int64_t nrows, const void* weights,
                                 RowsArgs a, int64_t max_rows, int sm_count, cudaStream_t s)
 {
-    constexpr int NT = 256, STAGES = 4;
     CUtensorMap wmap;
     RowMaps rmap;
     cudaError_t e;
@@ -574,16 +623,15 @@ cudaError_t launch_rows_product(int epi, const void* rows_in, int64_t nrows, con
         e = encode_tiles(&rmap.box[b], rows_in, 2, dims, str, box);
         if (e != cudaSuccess) return e;
     }
-    a.mt = (int)((epi == kRowsGateUp ? 2 * F : M) + kTileM - 1) / kTileM;
+    a.mt = (int)(((epi == kRowsGateUp ? 2 * F : M) + 2 * kTileM - 1) / (2 * kTileM));
     // an upper bound of the tiles: every expert with rows ends in a partial tile
-    const int64_t bound = (int64_t)a.mt * ((max_rows < a.E ? max_rows : a.E) + max_rows / NT);
+    const int64_t bound = (int64_t)a.mt * ((max_rows < a.E ? max_rows : a.E) + max_rows / kTileN);
     if (bound > INT32_MAX) return cudaErrorInvalidValue;  // tiles are counted in 32 bits
-    const int grid = (int)(bound < sm_count ? bound : sm_count);
     switch (epi) {
-        case kRowsGateUp: return launch_rows<kRowsGateUp, NT, STAGES>(wmap, rmap, a, grid, s);
-        case kRowsStore: return launch_rows<kRowsStore, NT, STAGES>(wmap, rmap, a, grid, s);
-        case kRowsDownBwd: return launch_rows<kRowsDownBwd, NT, STAGES>(wmap, rmap, a, grid, s);
-        default: return launch_rows<kRowsStoreT, NT, STAGES>(wmap, rmap, a, grid, s);
+        case kRowsGateUp: return launch_pairs(rows_kernel<kRowsGateUp>, bound, sm_count, s, wmap, rmap, a);
+        case kRowsStore: return launch_pairs(rows_kernel<kRowsStore>, bound, sm_count, s, wmap, rmap, a);
+        case kRowsDownBwd: return launch_pairs(rows_kernel<kRowsDownBwd>, bound, sm_count, s, wmap, rmap, a);
+        default: return launch_pairs(rows_kernel<kRowsStoreT>, bound, sm_count, s, wmap, rmap, a);
     }
 }
 
@@ -597,15 +645,11 @@ cudaError_t launch_weight_grad(const void* arows, const void* brows, int64_t nro
     cudaError_t e = encode_tiles(&amap, arows, 2, ad, as, box);
     if (e == cudaSuccess) e = encode_tiles(&bmap, brows, 2, bd, bs, box);
     if (e != cudaSuccess) return e;
-    a.mt = (a.M + kTileM - 1) / kTileM;
-    a.nt = (a.N + kGradN - 1) / kGradN;
+    a.mt = (a.M + 2 * kTileM - 1) / (2 * kTileM);
+    a.nt = (a.N + kTileN - 1) / kTileN;
     const int64_t total = (int64_t)a.mt * a.nt * a.E;
-    const int grid = (int)(total < sm_count ? total : sm_count);
-    constexpr int smem = kGradStages * (kTileM + kGradN) * kKB * 2 + 1024;
-    void (*k)(CUtensorMap, CUtensorMap, GradArgs) = f32 ? grad_kernel<true> : grad_kernel<false>;
-    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    return launch_pdl_smem(k, dim3(grid), dim3(kThreads), smem, s, amap, bmap, a);
+    return f32 ? launch_pairs(grad_kernel<true>, total, sm_count, s, amap, bmap, a)
+               : launch_pairs(grad_kernel<false>, total, sm_count, s, amap, bmap, a);
 }
 
 cudaError_t encode_tiles(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
