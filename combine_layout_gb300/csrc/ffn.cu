@@ -12,12 +12,21 @@
 // would cost as much as one with 128.  The pair halves what a CTA stages of the tokens: 32 KB for
 // 128 x 256 x 64 products per CTA where a CTA alone stages 48 KB.
 //
-// Roles of a CTA (192 threads): one thread loads its operand tiles by TMA into a
+// Roles of a CTA (320 threads): one thread loads its operand tiles by TMA into a
 // ring of shared-memory stages, one thread of the pair's first CTA issues the
-// products, four warps read the fp32 accumulators from tensor memory, apply the activation and
-// store bf16.  The accumulators are double-buffered, so a tile's epilogue runs
+// products, eight warps read the fp32 accumulators from tensor memory, apply the
+// activation and store bf16.  The accumulators are double-buffered, so a tile's epilogue runs
 // under the next tile's products.  CTAs are persistent; the tile list is
 // derived on the device from the layout's counts (no host synchronisation).
+//
+// Epilogue.  The accumulators hold features along tensor memory's lanes, the
+// outputs along a row.  They are read as 8 x 8 fragments, rounded in pairs and
+// transposed on the way through a warp's own piece of shared memory
+// (stmatrix.trans), from where 16-byte vectors go to the rows; the backward
+// pass's gate and up values come in the same way (cp.async, ldmatrix.trans).
+// Storing each lane's values directly, two bytes at a time, took some 24
+// instructions a column and bound the kernels (8 experts x 512 rows x 4096 x
+// 2048, down: 58 us; the products alone need 36).
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -27,34 +36,27 @@
 namespace moeep {
 namespace {
 
-constexpr int kThreads = 192;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kKB = 64;      // contraction elements per stage (128 bytes of bf16)
 constexpr int kTileM = 128;  // weight rows per CTA, 256 per pair
 constexpr int kTileN = 256;  // receive rows per tile, at most
-constexpr int kStages = 6;
+constexpr int kChunk = 32;   // receive rows (accumulator columns) an epilogue warp takes at a time
 constexpr int kBand = 8;     // n tiles that share the weights of one pass over an expert
 
 // Shared-memory control block of a CTA.
 template <int STAGES>
 struct Control {
-    uint64_t full[STAGES], empty[STAGES], ready[STAGES];
+    uint64_t full[STAGES], empty[STAGES], tail[STAGES], ready[STAGES];
     uint64_t acc_full[2], acc_empty[2];
     uint64_t drain;
     uint32_t tmem;
     volatile int dead;  // a bounded wait gave up
     int part[kThreads / 32];
     int cnt[kMaxExperts];
+    int off[kMaxExperts];      // first receive row of each expert
     int pre[kMaxExperts + 1];  // n tiles before each expert
 };
-
-// One whole 32-byte sector.
-__device__ __forceinline__ void store32(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e,
-                                        uint32_t f, uint32_t g, uint32_t h)
-{
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a), "r"(b), "r"(c),
-                 "r"(d), "r"(e), "r"(f), "r"(g), "r"(h)
-                 : "memory");
-}
 
 __device__ __forceinline__ void give_up(volatile int* dead, unsigned* err)
 {
@@ -62,19 +64,21 @@ __device__ __forceinline__ void give_up(volatile int* dead, unsigned* err)
     *(volatile unsigned*)(err + kErrTimeout) = 1u;
 }
 
-// Counts and the exclusive prefix of the experts' n tiles (rows / nt, rounded
-// up); all threads of the CTA.
-__device__ __forceinline__ void tile_prefix(const int32_t* __restrict__ cnt, int E, int nt, int* s_cnt,
-                                            int* s_pre, int* s_part)
+// Counts, first rows, and the exclusive prefix of the experts' n tiles (rows /
+// nt, rounded up); all threads of the CTA.
+template <int STAGES, typename Args>
+__device__ __forceinline__ void tile_prefix(Control<STAGES>& c, const Args& a, int nt)
 {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, E = a.E;
+    int *s_cnt = c.cnt, *s_pre = c.pre, *s_part = c.part;
     const int per = (E + kThreads - 1) / kThreads;
     const int lo = min(tid * per, E), hi = min(lo + per, E);
     int sum = 0;
     for (int e = lo; e < hi; ++e) {
-        const int c = __ldg(cnt + e);
-        s_cnt[e] = c;
-        sum += (c + nt - 1) / nt;
+        const int n = __ldg(a.cnt + e);
+        s_cnt[e] = n;
+        c.off[e] = a.mode == MOE_EP_HT ? __ldg(a.off + e) : e * a.S;
+        sum += (n + nt - 1) / nt;
     }
     int incl = sum;
 #pragma unroll
@@ -104,8 +108,10 @@ struct Tile {
     int rows;      // valid rows
     int n;         // rows of the product (a multiple of 32)
 
-    __device__ __forceinline__ void find(int i, const int* cnt, const int* pre, int mt, const RowsArgs& a)
+    template <int STAGES>
+    __device__ __forceinline__ void find(int i, const Control<STAGES>& ctl, int mt)
     {
+        const int *cnt = ctl.cnt, *pre = ctl.pre;
         while (pre[e + 1] * mt <= i) ++e;
         const int nt = pre[e + 1] - pre[e], c = cnt[e];
         const int r = i - pre[e] * mt;
@@ -118,7 +124,7 @@ struct Tile {
         const int w = ((c + nt - 1) / nt + 31) & ~31;
         rows = min(w, c - j * w);
         n = (rows + 31) & ~31;
-        row = (a.mode == MOE_EP_HT ? __ldg(a.off + e) : e * a.S) + j * w;
+        row = ctl.off[e] + j * w;
     }
 };
 
@@ -138,67 +144,156 @@ __device__ __forceinline__ float act(float g, int kind, float& slope)
     return g * cdf;
 }
 
-// Epilogues: sixteen accumulator columns (receive rows r0 + c0 ..) of the
-// warp's 32 tile rows.
-__device__ __forceinline__ void epi_store(const float (&v)[16], const RowsArgs& a, size_t row, int left,
-                                          int m)
+// A warp's piece of shared memory holds up to kChunk receive rows of `units`
+// 16-byte units (8 features); units are permuted so that neither the matrix
+// stores (8 rows of one unit) nor the row reads collide on banks.
+template <int UNITS>
+__device__ __forceinline__ uint32_t staged(uint32_t base, int row, int unit)
 {
-    if (m >= a.M) return;
-    __nv_bfloat16* p = a.out + row * a.M + m;
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        if (i < left) p[(size_t)i * a.M] = __float2bfloat16_rn(v[i]);
+    return base + row * (UNITS * 16) + ((unit ^ ((row / (8 / UNITS)) & (UNITS - 1))) << 4);
+}
+template <int UNITS>
+__device__ __forceinline__ uint32_t lane_address(uint32_t base, int unit0)
+{
+    // matrix l / 8 covers rows 8 (l / 8) .., its column l % 8 is a row
+    return staged<UNITS>(base, threadIdx.x & 31, unit0);
 }
 
-// Tile rows alternate 8 gate and 8 up features, so a feature's gate and up
-// values sit 8 lanes apart: of two neighbouring columns the gate lane takes
-// the first and the up lane the second, after one exchange.
-__device__ __forceinline__ void epi_gate_up(const float (&v)[16], const RowsArgs& a, size_t row, int left,
-                                            int f, int up)
+// The staged rows to global memory: `left` rows, features f0 .. limit.
+template <int UNITS>
+__device__ __forceinline__ void write_rows(uint32_t base, __nv_bfloat16* out, size_t ld, int left, int f0, int limit)
 {
-    const bool ok = f < a.F;
-    if (a.keep && ok) {
-        __nv_bfloat16* p = a.keep + row * 2 * a.F + (up ? a.F : 0) + f;
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (i < left) p[(size_t)i * 2 * a.F] = __float2bfloat16_rn(v[i]);
-    }
-    __nv_bfloat16* h = a.out + (row + up) * a.F + f;
-#pragma unroll
-    for (int i = 0; i < 16; i += 2) {
-        const float got = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + 1], 8);
-        const float g = up ? got : v[i], u = up ? v[i + 1] : got;
-        float slope;
-        const float r = act<false>(g, a.act, slope) * u;
-        if (ok && i + up < left) h[(size_t)i * a.F] = __float2bfloat16_rn(r);
+    for (int i = 0; i < UNITS; ++i) {
+        const int x = i * 32 + lane, row = x / UNITS, unit = x % UNITS;
+        const uint4 v = lds128(staged<UNITS>(base, row, unit));
+        if (row < left && f0 + unit * 8 < limit) *reinterpret_cast<uint4*>(out + row * ld + f0 + unit * 8) = v;
     }
 }
 
-// d hid (the accumulators) to d gate, d up, and the product of the forward
-// pass again.
-__device__ __forceinline__ void epi_down_bwd(const float (&v)[16], const RowsArgs& a, size_t row, int left,
-                                             int f)
+__device__ __forceinline__ uint32_t pack2(float a, float b)
 {
-    if (f >= a.F) return;
-    const __nv_bfloat16* gp = a.gate_up + row * 2 * a.F + f;
-    __nv_bfloat16* dp = a.out + row * 2 * a.F + f;
-    __nv_bfloat16 g[16], u[16];
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float low(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float high(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+
+// Epilogues of kChunk receive rows (from `row`, `left` of them valid) and the
+// warp's 32 weight rows; r[h] holds weight rows 16 h .. 16 h + 15.
+__device__ __forceinline__ void epi_store(const uint32_t (&r)[2][16], const RowsArgs& a, uint32_t stage, size_t row,
+                                          int left, int m0)
+{
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-        if (i < left) {
-            g[i] = gp[(size_t)i * 2 * a.F];
-            u[i] = gp[(size_t)i * 2 * a.F + a.F];
-        }
+    for (int u = 0; u < 4; ++u) {  // 8 features
+        const uint32_t(&q)[16] = r[u / 2];
+        const int o = (u & 1) * 2;
+        uint32_t p[4];
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-        if (i < left) {
-            const float gf = __bfloat162float(g[i]), uf = __bfloat162float(u[i]);
+        for (int i = 0; i < 4; ++i) p[i] = pack2(__uint_as_float(q[4 * i + o]), __uint_as_float(q[4 * i + o + 1]));
+        stmatrix_t(lane_address<4>(stage, u), p[0], p[1], p[2], p[3]);
+    }
+    __syncwarp();
+    write_rows<4>(stage, a.out + row * a.M, a.M, left, m0, a.M);
+    __syncwarp();
+}
+
+// Weight rows alternate 8 gate and 8 up features, so a fragment holds a
+// feature's gate and up values of the same receive rows.
+__device__ __forceinline__ void epi_gate_up(const uint32_t (&r)[2][16], const RowsArgs& a, uint32_t stage, size_t row,
+                                            int left, int f0)
+{
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        uint32_t ph[4], pg[4], pu[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float g0 = __uint_as_float(r[u][4 * i]), g1 = __uint_as_float(r[u][4 * i + 1]);
+            const float u0 = __uint_as_float(r[u][4 * i + 2]), u1 = __uint_as_float(r[u][4 * i + 3]);
             float slope;
-            const float av = act<true>(gf, a.act, slope);
-            dp[(size_t)i * 2 * a.F] = __float2bfloat16_rn(v[i] * uf * slope);
-            dp[(size_t)i * 2 * a.F + a.F] = __float2bfloat16_rn(v[i] * av);
-            if (a.keep) a.keep[(row + i) * a.F + f] = __float2bfloat16_rn(av * uf);
+            ph[i] = pack2(act<false>(g0, a.act, slope) * u0, act<false>(g1, a.act, slope) * u1);
+            pg[i] = pack2(g0, g1);
+            pu[i] = pack2(u0, u1);
         }
+        stmatrix_t(lane_address<2>(stage, u), ph[0], ph[1], ph[2], ph[3]);
+        if (a.keep) {
+            stmatrix_t(lane_address<2>(stage + 1024, u), pg[0], pg[1], pg[2], pg[3]);
+            stmatrix_t(lane_address<2>(stage + 2048, u), pu[0], pu[1], pu[2], pu[3]);
+        }
+    }
+    __syncwarp();
+    write_rows<2>(stage, a.out + row * a.F, a.F, left, f0, a.F);
+    if (a.keep) {
+        __nv_bfloat16* p = a.keep + row * 2 * a.F;
+        write_rows<2>(stage + 1024, p, 2 * (size_t)a.F, left, f0, a.F);
+        write_rows<2>(stage + 2048, p + a.F, 2 * (size_t)a.F, left, f0, a.F);
+    }
+    __syncwarp();
+}
+
+// The kept gate and up values of a chunk into `stage` (2 KB each), one copy
+// group; rows and features outside are skipped.
+__device__ __forceinline__ void fetch_gate_up(const RowsArgs& a, uint32_t stage, size_t row, int left, int f0)
+{
+    const int lane = threadIdx.x & 31;
+    const __nv_bfloat16* p = a.gate_up + row * 2 * a.F;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int x = i * 32 + lane, rr = x >> 2, unit = x & 3, f = f0 + unit * 8;
+        if (rr < left && f < a.F) {
+            const __nv_bfloat16* src = p + (size_t)rr * 2 * a.F + f;
+            cp_async16(staged<4>(stage, rr, unit), src);
+            cp_async16(staged<4>(stage + 2048, rr, unit), src + a.F);
+        }
+    }
+    cp_async_commit();
+}
+
+// d hid (the accumulators) to d gate, d up -- in place of the fetched gate and
+// up values -- and the forward pass's product again.
+__device__ __forceinline__ void epi_down_bwd(const uint32_t (&r)[2][16], const RowsArgs& a, uint32_t stage,
+                                             uint32_t stage_h, size_t row, int left, int f0)
+{
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const uint32_t(&q)[16] = r[u / 2];
+        const int o = (u & 1) * 2;
+        const uint32_t ag = lane_address<4>(stage, u), au = lane_address<4>(stage + 2048, u);
+        uint32_t g[4], v[4], h[4];
+        ldmatrix_t(ag, g[0], g[1], g[2], g[3]);
+        ldmatrix_t(au, v[0], v[1], v[2], v[3]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float d0 = __uint_as_float(q[4 * i + o]), d1 = __uint_as_float(q[4 * i + o + 1]);
+            float s0, s1;
+            const float a0 = act<true>(low(g[i]), a.act, s0), a1 = act<true>(high(g[i]), a.act, s1);
+            const float u0 = low(v[i]), u1 = high(v[i]);
+            h[i] = pack2(a0 * u0, a1 * u1);
+            g[i] = pack2(d0 * u0 * s0, d1 * u1 * s1);
+            v[i] = pack2(d0 * a0, d1 * a1);
+        }
+        __syncwarp();
+        stmatrix_t(ag, g[0], g[1], g[2], g[3]);
+        stmatrix_t(au, v[0], v[1], v[2], v[3]);
+        if (a.keep) stmatrix_t(lane_address<4>(stage_h, u), h[0], h[1], h[2], h[3]);
+    }
+    __syncwarp();
+    __nv_bfloat16* p = a.out + row * 2 * a.F;
+    write_rows<4>(stage, p, 2 * (size_t)a.F, left, f0, a.F);
+    write_rows<4>(stage + 2048, p + a.F, 2 * (size_t)a.F, left, f0, a.F);
+    if (a.keep) write_rows<4>(stage_h, a.keep + row * a.F, a.F, left, f0, a.F);
+    __syncwarp();
+}
+
+// Stages of the ring, and an epilogue warp's piece of shared memory: what is
+// left of 227 KB beside it.
+constexpr int rows_stages(int epi) { return epi == kRowsDownBwd ? 4 : 6; }
+constexpr int rows_stage_bytes(int epi) { return epi == kRowsDownBwd ? 10240 : epi == kRowsGateUp ? 3072 : 2048; }
+constexpr int kStageBytes = (kTileM + kTileN / 2) * kKB * 2;  // a CTA's 128 rows of each operand
+constexpr int rows_smem(int epi)
+{
+    return 1024 + rows_stages(epi) * kStageBytes + kEpiWarps * rows_stage_bytes(epi);
 }
 
 // Barriers, tensor memory and the pair; every thread of both CTAs.
@@ -209,11 +304,12 @@ __device__ __forceinline__ void start_pair(Control<STAGES>& c, int warp)
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(smem_u32(&c.full[i]), 1);
             mbar_init(smem_u32(&c.empty[i]), 1);
+            mbar_init(smem_u32(&c.tail[i]), 1);
             mbar_init(smem_u32(&c.ready[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&c.acc_full[i]), 1);
-            mbar_init(smem_u32(&c.acc_empty[i]), 8);  // the epilogue warps of both CTAs
+            mbar_init(smem_u32(&c.acc_empty[i]), 2 * kEpiWarps);  // the epilogue warps of both CTAs
         }
         mbar_init(smem_u32(&c.drain), 1);
         c.dead = 0;
@@ -262,8 +358,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const RowsArgs a)
 {
     constexpr bool A_MN = EPI == kRowsDownBwd || EPI == kRowsStoreT;
-    constexpr int STAGES = kStages;
-    constexpr int kABytes = kTileM * kKB * 2, kStageBytes = kABytes + kTileN / 2 * kKB * 2;
+    constexpr int STAGES = rows_stages(EPI);
+    constexpr int kABytes = kTileM * kKB * 2;
     extern __shared__ uint8_t dyn[];
     __shared__ Control<STAGES> c;
     const int warp = threadIdx.x >> 5;
@@ -272,7 +368,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     start_pair(c, warp);
     griddep_wait();
-    tile_prefix(a.cnt, a.E, kTileN, c.cnt, c.pre, c.part);
+    tile_prefix(c, a, kTileN);
     const int total = c.pre[a.E] * a.mt, first = blockIdx.x >> 1, step = gridDim.x >> 1;
     const int kblocks = (a.K + kKB - 1) / kKB;
 
@@ -282,7 +378,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             Tile t;
             bool ok = true;
             for (int i = first; i < total && ok; i += step) {
-                t.find(i, c.cnt, c.pre, a.mt, a);
+                t.find(i, c, a.mt);
                 const int m = t.m * 2 + (int)rank, half = t.n / 2, row = t.row + (int)rank * half;
                 for (int kb = 0; kb < kblocks; ++kb, ++it) {
                     const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
@@ -318,7 +414,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             Tile t;
             bool ok = true;
             for (int i = first; i < total && ok; i += step, ++tile) {
-                t.find(i, c.cnt, c.pre, a.mt, a);
+                t.find(i, c, a.mt);
                 const uint32_t acc = tile & 1u;
                 if (!mbar_wait(smem_u32(&c.acc_empty[acc]), ((tile >> 1) & 1u) ^ 1u, &c.dead)) {
                     ok = false;
@@ -347,35 +443,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (!ok) drain_products(c, a.err);
         }
     } else {
-        const int lane = threadIdx.x & 31, quarter = warp & 3;  // tensor-memory lanes of this warp
+        // two warps for each quarter of tensor memory's lanes, taking chunks in turn
+        const int lane = threadIdx.x & 31, quarter = warp & 3, side = (warp - 2) >> 2;
+        const uint32_t stage = ring + STAGES * kStageBytes + (warp - 2) * rows_stage_bytes(EPI);
         uint32_t tile = 0;
         Tile t;
         for (int i = first; i < total; i += step, ++tile) {
-            t.find(i, c.cnt, c.pre, a.mt, a);
+            t.find(i, c, a.mt);
             const uint32_t acc = tile & 1u;
+            const int m0 = (t.m * 2 + (int)rank) * kTileM + quarter * 32;  // first weight row
+            const int f0 = EPI == kRowsGateUp ? m0 / 2 : m0;                // first feature
+            int n0 = side * kChunk, buf = 0;
+            if (EPI == kRowsDownBwd && n0 < t.n) fetch_gate_up(a, stage, (size_t)(t.row + n0), t.rows - n0, f0);
             if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&c.acc_full[acc]), (tile >> 1) & 1u, &c.dead))) {
                 if (lane == 0) give_up(&c.dead, a.err);
                 break;
             }
             tc_fence_after();
             const uint32_t src = c.tmem + acc * kTileN + ((uint32_t)(quarter * 32) << 16);
-            const int r = (t.m * 2 + (int)rank) * kTileM + quarter * 32 + lane;  // weight row
-            for (int c0 = 0; c0 < t.n; c0 += 16) {
-                float v[16];
-                tmem_ld16(src + c0, v);
-                const size_t row = (size_t)(t.row + c0);
-                const int left = t.rows - c0;
-                if (EPI == kRowsGateUp)
-                    epi_gate_up(v, a, row, left, (r >> 4) * 8 + (r & 7), (r >> 3) & 1);
-                else if (EPI == kRowsDownBwd)
-                    epi_down_bwd(v, a, row, left, r);
-                else
-                    epi_store(v, a, row, left, r);
+            const uint32_t release = in_cta(smem_u32(&c.acc_empty[acc]), 0);
+            if (n0 >= t.n && lane == 0) mbar_arrive_relaxed(release);
+            for (; n0 < t.n; n0 += 2 * kChunk, buf ^= 1) {
+                const int next = n0 + 2 * kChunk;
+                uint32_t r[2][16];
+                __syncwarp();
+                tmem_ld_frag(src + n0, r[0]);
+                tmem_ld_frag(src + n0 + (16u << 16), r[1]);
+                if (EPI == kRowsDownBwd && next < t.n)
+                    fetch_gate_up(a, stage + (buf ^ 1) * 4096, (size_t)(t.row + next), t.rows - next, f0);
+                tmem_wait();
+                if (next >= t.n) {  // the accumulators are free for the next tile but one
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_relaxed(release);
+                }
+                const size_t row = (size_t)(t.row + n0);
+                const int left = t.rows - n0;
+                if (EPI == kRowsGateUp) {
+                    epi_gate_up(r, a, stage, row, left, f0);
+                } else if (EPI == kRowsDownBwd) {
+                    if (next < t.n) cp_async_wait<1>(); else cp_async_wait<0>();
+                    __syncwarp();
+                    epi_down_bwd(r, a, stage + buf * 4096, stage + 8192, row, left, f0);
+                } else {
+                    epi_store(r, a, stage, row, left, m0);
+                }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(in_cta(smem_u32(&c.acc_empty[acc]), 0));
         }
+        if (EPI == kRowsDownBwd) cp_async_wait<0>();
     }
     end_pair(c, warp);
 }
@@ -387,61 +502,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // block of an expert's rows may reach into rows that are not its own (the next
 // expert's, or slots that were never written): those rows of both operands are
 // cleared in shared memory before the product, because 0 x NaN would not be 0.
-// For that each CTA's copies are counted on its own barrier; the second CTA's
-// issuing warp clears its rows and passes the block on to the first one's
-// (`ready`), which clears its own and issues.
-template <bool F32>
-__device__ __forceinline__ void store_grad(const float (&v)[16], const GradArgs& a, size_t at, int n, bool wide)
-{
-    if (F32) {
-        float* p = (float*)a.dw + at;
-        float x[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = v[i];
-        if (a.accumulate) {
-#pragma unroll
-            for (int i = 0; i < 16; i += 4)
-                if (i < n) {
-                    const float4 o = *reinterpret_cast<const float4*>(p + i);
-                    x[i] += o.x; x[i + 1] += o.y; x[i + 2] += o.z; x[i + 3] += o.w;
-                }
-        }
-#pragma unroll
-        for (int i = 0; i < 16; i += 8)
-            if (i < n) {
-                if (wide) {
-                    store32(p + i, __float_as_uint(x[i]), __float_as_uint(x[i + 1]), __float_as_uint(x[i + 2]),
-                            __float_as_uint(x[i + 3]), __float_as_uint(x[i + 4]), __float_as_uint(x[i + 5]),
-                            __float_as_uint(x[i + 6]), __float_as_uint(x[i + 7]));
-                } else {
-                    *reinterpret_cast<float4*>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-                    *reinterpret_cast<float4*>(p + i + 4) = make_float4(x[i + 4], x[i + 5], x[i + 6], x[i + 7]);
-                }
-            }
-    } else {
-        __nv_bfloat16* p = (__nv_bfloat16*)a.dw + at;
-        uint32_t o[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-            o[i] = *reinterpret_cast<const uint32_t*>(&b);
-        }
-        if (wide && n >= 16) {
-            store32(p, o[0], o[1], o[2], o[3], o[4], o[5], o[6], o[7]);
-        } else {
-            *reinterpret_cast<uint4*>(p) = make_uint4(o[0], o[1], o[2], o[3]);
-            if (n >= 16) *reinterpret_cast<uint4*>(p + 8) = make_uint4(o[4], o[5], o[6], o[7]);
-        }
-    }
-}
+// For such a block each CTA's copies are counted on a barrier of its own (`tail`);
+// the second CTA's issuing warp clears its rows and passes the block on to the
+// first one's (`ready`), which clears its own and issues.  All other blocks are
+// counted on the first CTA's barrier: handing every block over cost a release
+// at cluster scope each (64 experts x 512 rows x 4096 x 4096: 1999 us).
+//
+// A warp's 32 x 64 (bf16) or 32 x 32 (fp32) piece of the gradient goes through
+// shared memory and out by TMA, which clips it at the matrix's edges; the
+// accumulating form adds in fp32 at the memory side (one addition per element
+// and call, so the result does not depend on their order).
+constexpr int kGradStages = 5;
+constexpr int kPiece = 4096;  // bytes of a piece: 32 rows of 128 bytes
 
 template <bool F32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     grad_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
-                const GradArgs a)
+                const __grid_constant__ CUtensorMap dmap, const GradArgs a)
 {
-    constexpr int STAGES = kStages;
-    constexpr int kABytes = kTileM * kKB * 2, kStageBytes = 2 * kABytes;
+    constexpr int STAGES = kGradStages;
+    constexpr int kABytes = kTileM * kKB * 2;
     constexpr int kBlock = 64 * kKB * 2;  // 64 features x 64 rows
     extern __shared__ uint8_t dyn[];
     __shared__ Control<STAGES> c;
@@ -450,6 +530,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t ring = (smem_u32(dyn) + 1023u) & ~1023u;
     start_pair(c, warp);
     griddep_wait();
+    tile_prefix(c, a, kTileN);
     const int per = a.mt * a.nt;
     const int64_t total = (int64_t)per * a.E, first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
@@ -461,30 +542,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const int e = (int)(i / per), q = (int)(i - (int64_t)e * per);
                 const int m0 = ((q / a.nt) * 2 + (int)rank) * kTileM;
                 const int n0 = (q % a.nt) * kTileN + (int)rank * (kTileN / 2);
-                const int rows = __ldg(a.cnt + e), base = a.mode == MOE_EP_HT ? __ldg(a.off + e) : e * a.S;
+                const int rows = c.cnt[e], base = c.off[e];
                 for (int r = 0; r < rows; r += kKB, ++it) {
                     const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
                     if (!mbar_wait(smem_u32(&c.empty[s]), ph ^ 1u, &c.dead)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t bar = smem_u32(&c.full[s]);
+                    const bool tail = rank != 0 && rows - r < kKB && (rows & 15) != 0;
+                    const uint32_t bar = tail ? smem_u32(&c.tail[s]) : in_cta(smem_u32(&c.full[s]), 0);
                     const uint32_t sa = ring + s * kStageBytes, sb = sa + kABytes;
-                    mbar_expect_tx(bar, kStageBytes);
+                    if (tail)
+                        mbar_expect_tx(bar, kStageBytes);
+                    else if (rank == 0)
+                        mbar_expect_tx(smem_u32(&c.full[s]),
+                                       rows - r < kKB && (rows & 15) != 0 ? kStageBytes : 2 * kStageBytes);
                     for (int b = 0; b < 2; ++b) {
                         tma_load(sa + b * kBlock, &amap, bar, m0 + b * 64, base + r);
                         tma_load(sb + b * kBlock, &bmap, bar, n0 + b * 64, base + r);
                     }
                 }
             }
-            if (!ok) drain_copies(c, it, a.err);
+            if (!ok) drain_copies(c, rank == 0 ? it : 0, a.err);
         }
     } else if (warp == 1) {
-        uint32_t it = 0, tile = 0;
+        uint32_t it = 0, tile = 0, phases = 0;  // phases: bit s, the phase of stage s's tail blocks
         bool ok = true;
         const uint32_t idesc = tc_idesc(2 * kTileM, kTileN, 1, 1);
         for (int64_t i = first; i < total && ok; i += step) {
-            const int rows = __ldg(a.cnt + (int)(i / per));
+            const int rows = c.cnt[(int)(i / per)];
             if (rows == 0) continue;
             const uint32_t acc = tile & 1u;
             if (rank == 0) {
@@ -496,29 +582,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint32_t d = c.tmem + acc * kTileN;
             for (int r = 0; r < rows; r += kKB, ++it) {
                 const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
-                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&c.full[s]), ph, &c.dead));
+                const int left = min(rows - r, kKB), steps = (left + 15) / 16;
+                const bool tail = left < steps * 16;
+                if (rank != 0 && !tail) continue;  // counted and issued by the first CTA
+                ok = __all_sync(0xffffffffu, rank == 0 ? mbar_wait(smem_u32(&c.full[s]), ph, &c.dead)
+                                                       : mbar_wait(smem_u32(&c.tail[s]), (phases >> s) & 1u, &c.dead));
                 if (!ok) break;
                 const uint32_t sa = ring + s * kStageBytes, sb = sa + kABytes;
-                const int left = min(rows - r, kKB), steps = (left + 15) / 16;
-                if (left < steps * 16) {
+                if (tail) {
                     // rows left .. steps * 16 of every 64-feature block (the
                     // swizzle moves 16-byte units within a row's 128 bytes only)
                     const int units = (steps * 16 - left) * 8;
                     for (int b = 0; b < kStageBytes / kBlock; ++b)
-                        for (int x = lane; x < units; x += 32)
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                             sa + b * kBlock + left * 128 + x * 16),
-                                         "r"(0)
-                                         : "memory");
+                        for (int x = lane; x < units; x += 32) sts128(sa + b * kBlock + left * 128 + x * 16, 0, 0, 0, 0);
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
+                    if (rank != 0) {
+                        if (lane == 0) mbar_arrive_cluster(in_cta(smem_u32(&c.ready[s]), 0));
+                    } else {
+                        ok = __all_sync(0xffffffffu,
+                                        mbar_wait<true>(smem_u32(&c.ready[s]), (phases >> s) & 1u, &c.dead));
+                        if (!ok) break;
+                    }
+                    phases ^= 1u << s;
+                    if (rank != 0) continue;
                 }
-                if (rank != 0) {
-                    if (lane == 0) mbar_arrive_cluster(in_cta(smem_u32(&c.ready[s]), 0));
-                    continue;
-                }
-                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&c.ready[s]), ph, &c.dead));
-                if (!ok) break;
                 tc_fence_after();
                 if (lane == 0) {
                     for (int k = 0; k < steps; ++k)
@@ -539,14 +627,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 give_up(&c.dead, a.err);
         }
     } else {
-        const int quarter = warp & 3;
-        // 32-byte stores need rows that start on 32 bytes
-        const bool wide = a.N % 16 == 0 && ((uintptr_t)a.dw & 31u) == 0;
+        const int quarter = warp & 3, side = (warp - 2) >> 2;
+        const uint32_t piece = ring + STAGES * kStageBytes + (warp - 2) * kPiece;
+        constexpr int kCols = F32 ? 32 : 64;
         uint32_t tile = 0;
         for (int64_t i = first; i < total; i += step) {
             const int e = (int)(i / per), q = (int)(i - (int64_t)e * per);
-            const int m = ((q / a.nt) * 2 + (int)rank) * kTileM + quarter * 32 + lane, n0 = (q % a.nt) * kTileN;
-            const bool some = __ldg(a.cnt + e) > 0;
+            const int m = ((q / a.nt) * 2 + (int)rank) * kTileM + quarter * 32, n0 = (q % a.nt) * kTileN;
+            const bool some = c.cnt[e] > 0;
             if (!some && a.accumulate) continue;
             const uint32_t acc = tile & 1u;
             if (some) {
@@ -558,39 +646,66 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tc_fence_after();
             }
             const uint32_t src = c.tmem + acc * kTileN + ((uint32_t)(quarter * 32) << 16);
-            const size_t at = ((size_t)e * a.M + m) * a.N + n0;
-            const int cols = min(kTileN, a.N - n0);
-            for (int c0 = 0; c0 < cols; c0 += 16) {
-                float v[16];
+            for (int c0 = side * kCols; c0 < kTileN; c0 += 2 * kCols) {
+                uint32_t v[kCols];
+                __syncwarp();
                 if (some) {
-                    tmem_ld16(src + c0, v);
+                    if (F32) {
+                        tmem_ld_rows(src + c0, reinterpret_cast<uint32_t(&)[32]>(v[0]));
+                    } else {
+                        tmem_ld_rows(src + c0, reinterpret_cast<uint32_t(&)[32]>(v[0]));
+                        tmem_ld_rows(src + c0 + 32, reinterpret_cast<uint32_t(&)[32]>(v[kCols - 32]));
+                    }
+                    tmem_wait();
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) v[j] = 0.f;
+                    for (int j = 0; j < kCols; ++j) v[j] = 0u;
                 }
-                if (m < a.M) store_grad<F32>(v, a, at + c0, cols - c0, wide);
-            }
-            if (some) {
-                tc_fence_before();
+                if (some && c0 + 2 * kCols >= kTileN) {  // the accumulators are free
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_relaxed(in_cta(smem_u32(&c.acc_empty[acc]), 0));
+                }
+                if (m >= a.M || n0 + c0 >= a.N) continue;
+                if (lane == 0) bulk_wait_read();  // the piece before has left
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(in_cta(smem_u32(&c.acc_empty[acc]), 0));
-                ++tile;
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    uint32_t o[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        o[j] = F32 ? v[4 * u + j]
+                                   : pack2(__uint_as_float(v[(8 * u + 2 * j) % kCols]),
+                                           __uint_as_float(v[(8 * u + 2 * j + 1) % kCols]));
+                    sts128(piece + lane * 128 + ((u ^ (lane & 7)) << 4), o[0], o[1], o[2], o[3]);
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) {
+                    if (F32 && a.accumulate)
+                        tma_add(&dmap, piece, n0 + c0, m, e);
+                    else
+                        tma_store(&dmap, piece, n0 + c0, m, e);
+                    bulk_commit();
+                }
             }
+            if (some) ++tile;
         }
+        if (lane == 0) bulk_wait();
+        __syncwarp();
     }
     end_pair(c, warp);
 }
 
-constexpr int kSmem = kStages * 2 * kTileM * kKB * 2 + 1024;
-
 template <typename... KArgs, typename... Args>
-cudaError_t launch_pairs(void (*k)(KArgs...), int64_t pairs, int sm_count, cudaStream_t s, const Args&... args)
+cudaError_t launch_pairs(void (*k)(KArgs...), int smem, int64_t pairs, int sm_count, cudaStream_t s,
+                         const Args&... args)
 {
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int most = sm_count / 2;
     const int n = (int)(pairs < most ? pairs : most);
-    return launch_pdl_smem(k, dim3(2 * n), dim3(kThreads), kSmem, s, args...);
+    return launch_pdl_smem(k, dim3(2 * n), dim3(kThreads), smem, s, args...);
 }
 
 }  // namespace
@@ -628,10 +743,10 @@ cudaError_t launch_rows_product(int epi, const void* rows_in, int64_t nrows, con
     const int64_t bound = (int64_t)a.mt * ((max_rows < a.E ? max_rows : a.E) + max_rows / kTileN);
     if (bound > INT32_MAX) return cudaErrorInvalidValue;  // tiles are counted in 32 bits
     switch (epi) {
-        case kRowsGateUp: return launch_pairs(rows_kernel<kRowsGateUp>, bound, sm_count, s, wmap, rmap, a);
-        case kRowsStore: return launch_pairs(rows_kernel<kRowsStore>, bound, sm_count, s, wmap, rmap, a);
-        case kRowsDownBwd: return launch_pairs(rows_kernel<kRowsDownBwd>, bound, sm_count, s, wmap, rmap, a);
-        default: return launch_pairs(rows_kernel<kRowsStoreT>, bound, sm_count, s, wmap, rmap, a);
+        case kRowsGateUp: return launch_pairs(rows_kernel<kRowsGateUp>, rows_smem(kRowsGateUp), bound, sm_count, s, wmap, rmap, a);
+        case kRowsStore: return launch_pairs(rows_kernel<kRowsStore>, rows_smem(kRowsStore), bound, sm_count, s, wmap, rmap, a);
+        case kRowsDownBwd: return launch_pairs(rows_kernel<kRowsDownBwd>, rows_smem(kRowsDownBwd), bound, sm_count, s, wmap, rmap, a);
+        default: return launch_pairs(rows_kernel<kRowsStoreT>, rows_smem(kRowsStoreT), bound, sm_count, s, wmap, rmap, a);
     }
 }
 
@@ -645,15 +760,23 @@ cudaError_t launch_weight_grad(const void* arows, const void* brows, int64_t nro
     cudaError_t e = encode_tiles(&amap, arows, 2, ad, as, box);
     if (e == cudaSuccess) e = encode_tiles(&bmap, brows, 2, bd, bs, box);
     if (e != cudaSuccess) return e;
+    CUtensorMap dmap;
+    const uint64_t es = f32 ? 4 : 2;
+    const uint64_t dd[3] = {(uint64_t)a.N, (uint64_t)a.M, (uint64_t)a.E};
+    const uint64_t ds[2] = {(uint64_t)a.N * es, (uint64_t)a.N * a.M * es};
+    const uint32_t dbox[3] = {(uint32_t)(128 / es), 32, 1};
+    e = encode_tiles(&dmap, a.dw, 3, dd, ds, dbox, f32 != 0);
+    if (e != cudaSuccess) return e;
     a.mt = (a.M + 2 * kTileM - 1) / (2 * kTileM);
     a.nt = (a.N + kTileN - 1) / kTileN;
     const int64_t total = (int64_t)a.mt * a.nt * a.E;
-    return f32 ? launch_pairs(grad_kernel<true>, total, sm_count, s, amap, bmap, a)
-               : launch_pairs(grad_kernel<false>, total, sm_count, s, amap, bmap, a);
+    constexpr int smem = 1024 + kGradStages * kStageBytes + kEpiWarps * kPiece;
+    return f32 ? launch_pairs(grad_kernel<true>, smem, total, sm_count, s, amap, bmap, dmap, a)
+               : launch_pairs(grad_kernel<false>, smem, total, sm_count, s, amap, bmap, dmap, a);
 }
 
 cudaError_t encode_tiles(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
-                         const uint64_t* strides, const uint32_t* box)
+                         const uint64_t* strides, const uint32_t* box, bool fp32)
 {
     using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
@@ -670,7 +793,7 @@ cudaError_t encode_tiles(CUtensorMap* map, const void* base, int rank, const uin
     }();
     if (!encode) return cudaErrorNotSupported;
     const cuuint32_t one[5] = {1, 1, 1, 1, 1};
-    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base),
+    const CUresult r = encode(map, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base),
                               reinterpret_cast<const cuuint64_t*>(dims),
                               reinterpret_cast<const cuuint64_t*>(strides), box, one,
                               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
