@@ -23,7 +23,7 @@
 // outputs along a row.  They are read as 8 x 8 fragments, rounded in pairs and
 // transposed on the way through a warp's own piece of shared memory
 // (stmatrix.trans), from where 16-byte vectors go to the rows; the backward
-// pass's gate and up values come in the same way (cp.async, ldmatrix.trans).
+// pass's gate and up values come in the same way (ldmatrix.trans).
 // Storing each lane's values directly, two bytes at a time, took some 24
 // instructions a column and bound the kernels (8 experts x 512 rows x 4096 x
 // 2048, down: 58 us; the products alone need 36).
@@ -38,6 +38,7 @@ namespace {
 
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kGradThreads = kThreads + 32;  // and a warp that clears rows
 constexpr int kKB = 64;      // contraction elements per stage (128 bytes of bf16)
 constexpr int kTileM = 128;  // weight rows per CTA, 256 per pair
 constexpr int kTileN = 256;  // receive rows per tile, at most
@@ -47,12 +48,12 @@ constexpr int kBand = 8;     // n tiles that share the weights of one pass over 
 // Shared-memory control block of a CTA.
 template <int STAGES>
 struct Control {
-    uint64_t full[STAGES], empty[STAGES], tail[STAGES], ready[STAGES];
+    uint64_t full[STAGES], empty[STAGES], tail[STAGES];
     uint64_t acc_full[2], acc_empty[2];
     uint64_t drain;
     uint32_t tmem;
     volatile int dead;  // a bounded wait gave up
-    int part[kThreads / 32];
+    int part[kGradThreads / 32];
     int cnt[kMaxExperts];
     int off[kMaxExperts];      // first receive row of each expert
     int pre[kMaxExperts + 1];  // n tiles before each expert
@@ -71,7 +72,7 @@ __device__ __forceinline__ void tile_prefix(Control<STAGES>& c, const Args& a, i
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, E = a.E;
     int *s_cnt = c.cnt, *s_pre = c.pre, *s_part = c.part;
-    const int per = (E + kThreads - 1) / kThreads;
+    const int threads = blockDim.x, per = (E + threads - 1) / threads;
     const int lo = min(tid * per, E), hi = min(lo + per, E);
     int sum = 0;
     for (int e = lo; e < hi; ++e) {
@@ -90,7 +91,7 @@ __device__ __forceinline__ void tile_prefix(Control<STAGES>& c, const Args& a, i
     __syncthreads();
     int run = incl - sum;
     for (int w = 0; w < warp; ++w) run += s_part[w];
-    if (tid == kThreads - 1) s_pre[E] = run + sum;
+    if (tid == threads - 1) s_pre[E] = run + sum;
     for (int e = lo; e < hi; ++e) {
         s_pre[e] = run;
         run += (s_cnt[e] + nt - 1) / nt;
@@ -128,7 +129,7 @@ struct Tile {
     }
 };
 
-__device__ __forceinline__ float sigmoid(float g) { return 1.f / (1.f + __expf(-g)); }
+__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
 
 // act(g) and its derivative.
 template <bool GRAD>
@@ -232,23 +233,32 @@ __device__ __forceinline__ void epi_gate_up(const uint32_t (&r)[2][16], const Ro
     __syncwarp();
 }
 
-// The kept gate and up values of a chunk into `stage` (2 KB each), one copy
-// group; rows and features outside are skipped.
-__device__ __forceinline__ void fetch_gate_up(const RowsArgs& a, uint32_t stage, size_t row, int left, int f0)
-{
-    const int lane = threadIdx.x & 31;
-    const __nv_bfloat16* p = a.gate_up + row * 2 * a.F;
+// The kept gate and up values of a chunk into registers, 16 bytes of four rows
+// each; rows and features outside are skipped.
+struct GateUpRows {
+    uint4 g[4], u[4];
+    __device__ __forceinline__ void fetch(const RowsArgs& a, size_t row, int left, int f0)
+    {
+        const int lane = threadIdx.x & 31, f = f0 + (lane & 3) * 8;
+        const __nv_bfloat16* p = a.gate_up + (row + (lane >> 2)) * 2 * a.F + f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int x = i * 32 + lane, rr = x >> 2, unit = x & 3, f = f0 + unit * 8;
-        if (rr < left && f < a.F) {
-            const __nv_bfloat16* src = p + (size_t)rr * 2 * a.F + f;
-            cp_async16(staged<4>(stage, rr, unit), src);
-            cp_async16(staged<4>(stage + 2048, rr, unit), src + a.F);
+        for (int i = 0; i < 4; ++i)
+            if (i * 8 + (lane >> 2) < left && f < a.F) {
+                g[i] = __ldg(reinterpret_cast<const uint4*>(p + (size_t)i * 16 * a.F));
+                u[i] = __ldg(reinterpret_cast<const uint4*>(p + (size_t)i * 16 * a.F + a.F));
+            }
+    }
+    __device__ __forceinline__ void put(uint32_t stage) const
+    {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t at = staged<4>(stage, i * 8 + (lane >> 2), lane & 3);
+            sts128(at, g[i].x, g[i].y, g[i].z, g[i].w);
+            sts128(at + 2048, u[i].x, u[i].y, u[i].z, u[i].w);
         }
     }
-    cp_async_commit();
-}
+};
 
 // d hid (the accumulators) to d gate, d up -- in place of the fetched gate and
 // up values -- and the forward pass's product again.
@@ -288,8 +298,8 @@ __device__ __forceinline__ void epi_down_bwd(const uint32_t (&r)[2][16], const R
 
 // Stages of the ring, and an epilogue warp's piece of shared memory: what is
 // left of 227 KB beside it.
-constexpr int rows_stages(int epi) { return epi == kRowsDownBwd ? 4 : 6; }
-constexpr int rows_stage_bytes(int epi) { return epi == kRowsDownBwd ? 10240 : epi == kRowsGateUp ? 3072 : 2048; }
+constexpr int rows_stages(int epi) { return epi == kRowsDownBwd ? 5 : 6; }
+constexpr int rows_stage_bytes(int epi) { return epi == kRowsDownBwd ? 6144 : epi == kRowsGateUp ? 3072 : 2048; }
 constexpr int kStageBytes = (kTileM + kTileN / 2) * kKB * 2;  // a CTA's 128 rows of each operand
 constexpr int rows_smem(int epi)
 {
@@ -298,14 +308,13 @@ constexpr int rows_smem(int epi)
 
 // Barriers, tensor memory and the pair; every thread of both CTAs.
 template <int STAGES>
-__device__ __forceinline__ void start_pair(Control<STAGES>& c, int warp)
+__device__ __forceinline__ void start_pair(Control<STAGES>& c, int warp, int full_arrivals)
 {
     if (threadIdx.x == 0) {
         for (int i = 0; i < STAGES; ++i) {
-            mbar_init(smem_u32(&c.full[i]), 1);
+            mbar_init(smem_u32(&c.full[i]), full_arrivals);
             mbar_init(smem_u32(&c.empty[i]), 1);
             mbar_init(smem_u32(&c.tail[i]), 1);
-            mbar_init(smem_u32(&c.ready[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&c.acc_full[i]), 1);
@@ -366,7 +375,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t rank = cluster_rank();
     const uint32_t ring = (smem_u32(dyn) + 1023u) & ~1023u;
 
-    start_pair(c, warp);
+    start_pair(c, warp, 1);
     griddep_wait();
     tile_prefix(c, a, kTileN);
     const int total = c.pre[a.E] * a.mt, first = blockIdx.x >> 1, step = gridDim.x >> 1;
@@ -453,8 +462,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint32_t acc = tile & 1u;
             const int m0 = (t.m * 2 + (int)rank) * kTileM + quarter * 32;  // first weight row
             const int f0 = EPI == kRowsGateUp ? m0 / 2 : m0;                // first feature
-            int n0 = side * kChunk, buf = 0;
-            if (EPI == kRowsDownBwd && n0 < t.n) fetch_gate_up(a, stage, (size_t)(t.row + n0), t.rows - n0, f0);
+            int n0 = side * kChunk;
+            GateUpRows kept;
+            if (EPI == kRowsDownBwd && n0 < t.n) kept.fetch(a, (size_t)(t.row + n0), t.rows - n0, f0);
             if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&c.acc_full[acc]), (tile >> 1) & 1u, &c.dead))) {
                 if (lane == 0) give_up(&c.dead, a.err);
                 break;
@@ -463,14 +473,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint32_t src = c.tmem + acc * kTileN + ((uint32_t)(quarter * 32) << 16);
             const uint32_t release = in_cta(smem_u32(&c.acc_empty[acc]), 0);
             if (n0 >= t.n && lane == 0) mbar_arrive_relaxed(release);
-            for (; n0 < t.n; n0 += 2 * kChunk, buf ^= 1) {
+            for (; n0 < t.n; n0 += 2 * kChunk) {
                 const int next = n0 + 2 * kChunk;
                 uint32_t r[2][16];
                 __syncwarp();
                 tmem_ld_frag(src + n0, r[0]);
                 tmem_ld_frag(src + n0 + (16u << 16), r[1]);
-                if (EPI == kRowsDownBwd && next < t.n)
-                    fetch_gate_up(a, stage + (buf ^ 1) * 4096, (size_t)(t.row + next), t.rows - next, f0);
+                if (EPI == kRowsDownBwd) {
+                    kept.put(stage);
+                    if (next < t.n) kept.fetch(a, (size_t)(t.row + next), t.rows - next, f0);
+                }
                 tmem_wait();
                 if (next >= t.n) {  // the accumulators are free for the next tile but one
                     tc_fence_before();
@@ -482,15 +494,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (EPI == kRowsGateUp) {
                     epi_gate_up(r, a, stage, row, left, f0);
                 } else if (EPI == kRowsDownBwd) {
-                    if (next < t.n) cp_async_wait<1>(); else cp_async_wait<0>();
                     __syncwarp();
-                    epi_down_bwd(r, a, stage + buf * 4096, stage + 8192, row, left, f0);
+                    epi_down_bwd(r, a, stage, stage + 4096, row, left, f0);
                 } else {
                     epi_store(r, a, stage, row, left, m0);
                 }
             }
         }
-        if (EPI == kRowsDownBwd) cp_async_wait<0>();
     }
     end_pair(c, warp);
 }
@@ -502,21 +512,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // block of an expert's rows may reach into rows that are not its own (the next
 // expert's, or slots that were never written): those rows of both operands are
 // cleared in shared memory before the product, because 0 x NaN would not be 0.
-// For such a block each CTA's copies are counted on a barrier of its own (`tail`);
-// the second CTA's issuing warp clears its rows and passes the block on to the
-// first one's (`ready`), which clears its own and issues.  All other blocks are
-// counted on the first CTA's barrier: handing every block over cost a release
-// at cluster scope each (64 experts x 512 rows x 4096 x 4096: 1999 us).
+// For such a block each CTA's copies are counted on a barrier of its own (`tail`),
+// and a warp of its own, running ahead of the products, clears the rows before
+// it arrives at the barrier that the issuing thread waits for.  (Clearing them
+// in the issuing warp took a quarter of the time: 32 experts x about 512 rows x
+// 4096 x 4096, 494 us against 392 without the clearing.)
 //
 // A warp's 32 x 64 (bf16) or 32 x 32 (fp32) piece of the gradient goes through
 // shared memory and out by TMA, which clips it at the matrix's edges; the
 // accumulating form adds in fp32 at the memory side (one addition per element
 // and call, so the result does not depend on their order).
 constexpr int kGradStages = 5;
+
+// A pair's tiles in turn (n fastest, then m, then the expert), without a
+// division a tile: the step is split once.
+struct GradTile {
+    int e, m, n;
+    int se, sm, sn, E, mt, nt;
+
+    __device__ __forceinline__ GradTile(const GradArgs& a, int first, int step) : E(a.E), mt(a.mt), nt(a.nt)
+    {
+        const int per = mt * nt;
+        e = first / per;
+        m = (first - e * per) / nt;
+        n = first - e * per - m * nt;
+        se = step / per;
+        sm = (step - se * per) / nt;
+        sn = step - se * per - sm * nt;
+    }
+    __device__ __forceinline__ bool valid() const { return e < E; }
+    __device__ __forceinline__ void next()
+    {
+        n += sn;
+        m += sm;
+        e += se;
+        if (n >= nt) {
+            n -= nt;
+            ++m;
+        }
+        if (m >= mt) {
+            m -= mt;
+            ++e;
+        }
+    }
+};
 constexpr int kPiece = 4096;  // bytes of a piece: 32 rows of 128 bytes
 
 template <bool F32>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
     grad_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
                 const __grid_constant__ CUtensorMap dmap, const GradArgs a)
 {
@@ -525,38 +568,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     constexpr int kBlock = 64 * kKB * 2;  // 64 features x 64 rows
     extern __shared__ uint8_t dyn[];
     __shared__ Control<STAGES> c;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5;
     const uint32_t rank = cluster_rank();
     const uint32_t ring = (smem_u32(dyn) + 1023u) & ~1023u;
-    start_pair(c, warp);
+    start_pair(c, warp, 2);
     griddep_wait();
     tile_prefix(c, a, kTileN);
-    const int per = a.mt * a.nt;
-    const int64_t total = (int64_t)per * a.E, first = blockIdx.x >> 1, step = gridDim.x >> 1;
+    const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
     if (warp == 0) {
         if (elect_one()) {
             uint32_t it = 0;
             bool ok = true;
-            for (int64_t i = first; i < total && ok; i += step) {
-                const int e = (int)(i / per), q = (int)(i - (int64_t)e * per);
-                const int m0 = ((q / a.nt) * 2 + (int)rank) * kTileM;
-                const int n0 = (q % a.nt) * kTileN + (int)rank * (kTileN / 2);
-                const int rows = c.cnt[e], base = c.off[e];
+            for (GradTile t(a, first, step); t.valid() && ok; t.next()) {
+                const int m0 = (t.m * 2 + (int)rank) * kTileM;
+                const int n0 = t.n * kTileN + (int)rank * (kTileN / 2);
+                const int rows = c.cnt[t.e], base = c.off[t.e];
                 for (int r = 0; r < rows; r += kKB, ++it) {
                     const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
                     if (!mbar_wait(smem_u32(&c.empty[s]), ph ^ 1u, &c.dead)) {
                         ok = false;
                         break;
                     }
-                    const bool tail = rank != 0 && rows - r < kKB && (rows & 15) != 0;
+                    const bool tail = rows - r < kKB && (rows & 15) != 0;
                     const uint32_t bar = tail ? smem_u32(&c.tail[s]) : in_cta(smem_u32(&c.full[s]), 0);
                     const uint32_t sa = ring + s * kStageBytes, sb = sa + kABytes;
                     if (tail)
                         mbar_expect_tx(bar, kStageBytes);
                     else if (rank == 0)
-                        mbar_expect_tx(smem_u32(&c.full[s]),
-                                       rows - r < kKB && (rows & 15) != 0 ? kStageBytes : 2 * kStageBytes);
+                        mbar_expect_tx(smem_u32(&c.full[s]), 2 * kStageBytes);
+                    else
+                        mbar_arrive_relaxed(bar);
                     for (int b = 0; b < 2; ++b) {
                         tma_load(sa + b * kBlock, &amap, bar, m0 + b * 64, base + r);
                         tma_load(sb + b * kBlock, &bmap, bar, n0 + b * 64, base + r);
@@ -566,74 +608,70 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (!ok) drain_copies(c, rank == 0 ? it : 0, a.err);
         }
     } else if (warp == 1) {
-        uint32_t it = 0, tile = 0, phases = 0;  // phases: bit s, the phase of stage s's tail blocks
-        bool ok = true;
-        const uint32_t idesc = tc_idesc(2 * kTileM, kTileN, 1, 1);
-        for (int64_t i = first; i < total && ok; i += step) {
-            const int rows = c.cnt[(int)(i / per)];
-            if (rows == 0) continue;
-            const uint32_t acc = tile & 1u;
-            if (rank == 0) {
-                ok = __all_sync(0xffffffffu,
-                                mbar_wait(smem_u32(&c.acc_empty[acc]), ((tile >> 1) & 1u) ^ 1u, &c.dead));
-                if (!ok) break;
-                tc_fence_after();
-            }
-            const uint32_t d = c.tmem + acc * kTileN;
-            for (int r = 0; r < rows; r += kKB, ++it) {
-                const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
-                const int left = min(rows - r, kKB), steps = (left + 15) / 16;
-                const bool tail = left < steps * 16;
-                if (rank != 0 && !tail) continue;  // counted and issued by the first CTA
-                ok = __all_sync(0xffffffffu, rank == 0 ? mbar_wait(smem_u32(&c.full[s]), ph, &c.dead)
-                                                       : mbar_wait(smem_u32(&c.tail[s]), (phases >> s) & 1u, &c.dead));
-                if (!ok) break;
-                const uint32_t sa = ring + s * kStageBytes, sb = sa + kABytes;
-                if (tail) {
-                    // rows left .. steps * 16 of every 64-feature block (the
-                    // swizzle moves 16-byte units within a row's 128 bytes only)
-                    const int units = (steps * 16 - left) * 8;
-                    for (int b = 0; b < kStageBytes / kBlock; ++b)
-                        for (int x = lane; x < units; x += 32) sts128(sa + b * kBlock + left * 128 + x * 16, 0, 0, 0, 0);
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
-                    if (rank != 0) {
-                        if (lane == 0) mbar_arrive_cluster(in_cta(smem_u32(&c.ready[s]), 0));
-                    } else {
-                        ok = __all_sync(0xffffffffu,
-                                        mbar_wait<true>(smem_u32(&c.ready[s]), (phases >> s) & 1u, &c.dead));
-                        if (!ok) break;
-                    }
-                    phases ^= 1u << s;
-                    if (rank != 0) continue;
+        if (rank == 0 && elect_one()) {
+            uint32_t it = 0, tile = 0;
+            bool ok = true;
+            const uint32_t idesc = tc_idesc(2 * kTileM, kTileN, 1, 1);
+            for (GradTile t(a, first, step); t.valid() && ok; t.next()) {
+                const int rows = c.cnt[t.e];
+                if (rows == 0) continue;
+                const uint32_t acc = tile & 1u;
+                if (!mbar_wait(smem_u32(&c.acc_empty[acc]), ((tile >> 1) & 1u) ^ 1u, &c.dead)) {
+                    ok = false;
+                    break;
                 }
                 tc_fence_after();
-                if (lane == 0) {
+                const uint32_t d = c.tmem + acc * kTileN;
+                for (int r = 0; r < rows; r += kKB, ++it) {
+                    const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
+                    const int steps = (min(rows - r, kKB) + 15) / 16;
+                    // the last block may have been written by the clearing warps
+                    if (!(rows - r <= kKB ? mbar_wait<true>(smem_u32(&c.full[s]), ph, &c.dead)
+                                          : mbar_wait(smem_u32(&c.full[s]), ph, &c.dead))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sa = ring + s * kStageBytes, sb = sa + kABytes;
                     for (int k = 0; k < steps; ++k)
                         tc_mma(d, tc_desc(sa + k * 2048, kBlock), tc_desc(sb + k * 2048, kBlock), idesc,
                                (r | k) != 0);
                     tc_commit(smem_u32(&c.empty[s]));
                 }
-                __syncwarp();
+                if (ok) tc_commit(smem_u32(&c.acc_full[acc]));
+                ++tile;
             }
-            if (ok && rank == 0 && lane == 0) tc_commit(smem_u32(&c.acc_full[acc]));
-            __syncwarp();
-            ++tile;
+            if (!ok) drain_products(c, a.err);
         }
-        if (!ok && lane == 0) {
-            if (rank == 0)
-                drain_products(c, a.err);
-            else
-                give_up(&c.dead, a.err);
+    } else if (warp == 2 + kEpiWarps) {
+        // clears rows left .. 16 steps of every 64-feature block (the swizzle
+        // moves 16-byte units within a row's 128 bytes only)
+        uint32_t it = 0, phases = 0;  // phases: bit s, the phase of stage s's tail blocks
+        const uint32_t lane = threadIdx.x & 31;
+        for (GradTile t(a, first, step); t.valid(); t.next()) {
+            const int rows = c.cnt[t.e], blocks = (rows + kKB - 1) / kKB;
+            it += blocks;
+            if ((rows & 15) == 0) continue;
+            const uint32_t s = (it - 1) % STAGES, sa = ring + s * kStageBytes;
+            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&c.tail[s]), (phases >> s) & 1u, &c.dead))) {
+                if (lane == 0) give_up(&c.dead, a.err);
+                break;
+            }
+            phases ^= 1u << s;
+            const int left = rows - (blocks - 1) * kKB, units = (((left + 15) & ~15) - left) * 8;
+            for (int b = 0; b < kStageBytes / kBlock; ++b)
+                for (int x = (int)lane; x < units; x += 32) sts128(sa + b * kBlock + left * 128 + x * 16, 0, 0, 0, 0);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(in_cta(smem_u32(&c.full[s]), 0));
         }
     } else {
-        const int quarter = warp & 3, side = (warp - 2) >> 2;
+        const int lane = threadIdx.x & 31, quarter = warp & 3, side = (warp - 2) >> 2;
         const uint32_t piece = ring + STAGES * kStageBytes + (warp - 2) * kPiece;
         constexpr int kCols = F32 ? 32 : 64;
         uint32_t tile = 0;
-        for (int64_t i = first; i < total; i += step) {
-            const int e = (int)(i / per), q = (int)(i - (int64_t)e * per);
-            const int m = ((q / a.nt) * 2 + (int)rank) * kTileM + quarter * 32, n0 = (q % a.nt) * kTileN;
+        for (GradTile t(a, first, step); t.valid(); t.next()) {
+            const int e = t.e, m = (t.m * 2 + (int)rank) * kTileM + quarter * 32, n0 = t.n * kTileN;
             const bool some = c.cnt[e] > 0;
             if (!some && a.accumulate) continue;
             const uint32_t acc = tile & 1u;
@@ -698,14 +736,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 template <typename... KArgs, typename... Args>
-cudaError_t launch_pairs(void (*k)(KArgs...), int smem, int64_t pairs, int sm_count, cudaStream_t s,
+cudaError_t launch_pairs(void (*k)(KArgs...), int threads, int smem, int64_t pairs, int sm_count, cudaStream_t s,
                          const Args&... args)
 {
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int most = sm_count / 2;
     const int n = (int)(pairs < most ? pairs : most);
-    return launch_pdl_smem(k, dim3(2 * n), dim3(kThreads), smem, s, args...);
+    return launch_pdl_smem(k, dim3(2 * n), dim3(threads), smem, s, args...);
 }
 
 }  // namespace
@@ -743,10 +781,10 @@ cudaError_t launch_rows_product(int epi, const void* rows_in, int64_t nrows, con
     const int64_t bound = (int64_t)a.mt * ((max_rows < a.E ? max_rows : a.E) + max_rows / kTileN);
     if (bound > INT32_MAX) return cudaErrorInvalidValue;  // tiles are counted in 32 bits
     switch (epi) {
-        case kRowsGateUp: return launch_pairs(rows_kernel<kRowsGateUp>, rows_smem(kRowsGateUp), bound, sm_count, s, wmap, rmap, a);
-        case kRowsStore: return launch_pairs(rows_kernel<kRowsStore>, rows_smem(kRowsStore), bound, sm_count, s, wmap, rmap, a);
-        case kRowsDownBwd: return launch_pairs(rows_kernel<kRowsDownBwd>, rows_smem(kRowsDownBwd), bound, sm_count, s, wmap, rmap, a);
-        default: return launch_pairs(rows_kernel<kRowsStoreT>, rows_smem(kRowsStoreT), bound, sm_count, s, wmap, rmap, a);
+        case kRowsGateUp: return launch_pairs(rows_kernel<kRowsGateUp>, kThreads, rows_smem(kRowsGateUp), bound, sm_count, s, wmap, rmap, a);
+        case kRowsStore: return launch_pairs(rows_kernel<kRowsStore>, kThreads, rows_smem(kRowsStore), bound, sm_count, s, wmap, rmap, a);
+        case kRowsDownBwd: return launch_pairs(rows_kernel<kRowsDownBwd>, kThreads, rows_smem(kRowsDownBwd), bound, sm_count, s, wmap, rmap, a);
+        default: return launch_pairs(rows_kernel<kRowsStoreT>, kThreads, rows_smem(kRowsStoreT), bound, sm_count, s, wmap, rmap, a);
     }
 }
 
@@ -770,9 +808,10 @@ cudaError_t launch_weight_grad(const void* arows, const void* brows, int64_t nro
     a.mt = (a.M + 2 * kTileM - 1) / (2 * kTileM);
     a.nt = (a.N + kTileN - 1) / kTileN;
     const int64_t total = (int64_t)a.mt * a.nt * a.E;
+    if (total > INT32_MAX) return cudaErrorInvalidValue;  // tiles are counted in 32 bits
     constexpr int smem = 1024 + kGradStages * kStageBytes + kEpiWarps * kPiece;
-    return f32 ? launch_pairs(grad_kernel<true>, smem, total, sm_count, s, amap, bmap, dmap, a)
-               : launch_pairs(grad_kernel<false>, smem, total, sm_count, s, amap, bmap, dmap, a);
+    return f32 ? launch_pairs(grad_kernel<true>, kGradThreads, smem, total, sm_count, s, amap, bmap, dmap, a)
+               : launch_pairs(grad_kernel<false>, kGradThreads, smem, total, sm_count, s, amap, bmap, dmap, a);
 }
 
 cudaError_t encode_tiles(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
