@@ -48,7 +48,8 @@ constexpr int kBand = 8;     // n tiles that share the weights of one pass over 
 // Shared-memory control block of a CTA.
 template <int STAGES>
 struct Control {
-    uint64_t full[STAGES], empty[STAGES], tail[STAGES];
+    uint64_t full[STAGES], empty[STAGES];
+    uint64_t tail_full[2], tail_ready[2], tail_empty[2];
     uint64_t acc_full[2], acc_empty[2];
     uint64_t drain;
     uint32_t tmem;
@@ -308,17 +309,19 @@ constexpr int rows_smem(int epi)
 
 // Barriers, tensor memory and the pair; every thread of both CTAs.
 template <int STAGES>
-__device__ __forceinline__ void start_pair(Control<STAGES>& c, int warp, int full_arrivals)
+__device__ __forceinline__ void start_pair(Control<STAGES>& c, int warp)
 {
     if (threadIdx.x == 0) {
         for (int i = 0; i < STAGES; ++i) {
-            mbar_init(smem_u32(&c.full[i]), full_arrivals);
+            mbar_init(smem_u32(&c.full[i]), 1);
             mbar_init(smem_u32(&c.empty[i]), 1);
-            mbar_init(smem_u32(&c.tail[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&c.acc_full[i]), 1);
             mbar_init(smem_u32(&c.acc_empty[i]), 2 * kEpiWarps);  // the epilogue warps of both CTAs
+            mbar_init(smem_u32(&c.tail_full[i]), 1);
+            mbar_init(smem_u32(&c.tail_ready[i]), 2);
+            mbar_init(smem_u32(&c.tail_empty[i]), 1);
         }
         mbar_init(smem_u32(&c.drain), 1);
         c.dead = 0;
@@ -375,7 +378,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t rank = cluster_rank();
     const uint32_t ring = (smem_u32(dyn) + 1023u) & ~1023u;
 
-    start_pair(c, warp, 1);
+    start_pair(c, warp);
     griddep_wait();
     tile_prefix(c, a, kTileN);
     const int total = c.pre[a.E] * a.mt, first = blockIdx.x >> 1, step = gridDim.x >> 1;
@@ -508,15 +511,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------------------
 // Weight gradients: dW[e] = sum over the expert's rows of a_row b_row^T.  Both
 // operands are read with their features contiguous (rows are the contraction);
-// a tile is 256 x 256 of one expert's gradient, 128 x 256 in each CTA.  The last
-// block of an expert's rows may reach into rows that are not its own (the next
-// expert's, or slots that were never written): those rows of both operands are
-// cleared in shared memory before the product, because 0 x NaN would not be 0.
-// For such a block each CTA's copies are counted on a barrier of its own (`tail`),
-// and a warp of its own, running ahead of the products, clears the rows before
-// it arrives at the barrier that the issuing thread waits for.  (Clearing them
-// in the issuing warp took a quarter of the time: 32 experts x about 512 rows x
-// 4096 x 4096, 494 us against 392 without the clearing.)
+// a tile is 256 x 256 of one expert's gradient, 128 x 256 in each CTA.
+//
+// The contraction runs in steps of 16 rows, and an expert's last step may reach
+// into rows that are not its own (the next expert's, or slots that were never
+// written): those rows of both operands are cleared in shared memory before the
+// product, because 0 x NaN would not be 0.  That step has a buffer of its own,
+// loaded at the start of the tile, and a warp of each CTA clears its rows while
+// the whole steps run.  (With the clearing in the ring's order its latency, about
+// a microsecond a tile, showed in full: 32 experts x about 512 rows x 4096 x 4096
+// 492 us, against 376 for 512 rows each.)
 //
 // A warp's 32 x 64 (bf16) or 32 x 32 (fp32) piece of the gradient goes through
 // shared memory and out by TMA, which clips it at the matrix's edges; the
@@ -557,10 +561,13 @@ struct GradTile {
     }
 };
 constexpr int kPiece = 4096;  // bytes of a piece: 32 rows of 128 bytes
+constexpr int kTailBlock = 64 * 16 * 2;       // 64 features x 16 rows
+constexpr int kTailBytes = 4 * kTailBlock;    // a CTA's 128 features of each operand
 
 template <bool F32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
     grad_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
+                const __grid_constant__ CUtensorMap atail, const __grid_constant__ CUtensorMap btail,
                 const __grid_constant__ CUtensorMap dmap, const GradArgs a)
 {
     constexpr int STAGES = kGradStages;
@@ -571,49 +578,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
     const int warp = threadIdx.x >> 5;
     const uint32_t rank = cluster_rank();
     const uint32_t ring = (smem_u32(dyn) + 1023u) & ~1023u;
-    start_pair(c, warp, 2);
+    start_pair(c, warp);
     griddep_wait();
     tile_prefix(c, a, kTileN);
     const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
+    const uint32_t tails = ring + STAGES * kStageBytes;  // two last steps
+
     if (warp == 0) {
         if (elect_one()) {
-            uint32_t it = 0;
+            uint32_t it = 0, nt = 0;  // blocks and last steps loaded
             bool ok = true;
             for (GradTile t(a, first, step); t.valid() && ok; t.next()) {
                 const int m0 = (t.m * 2 + (int)rank) * kTileM;
                 const int n0 = t.n * kTileN + (int)rank * (kTileN / 2);
-                const int rows = c.cnt[t.e], base = c.off[t.e];
-                for (int r = 0; r < rows; r += kKB, ++it) {
+                const int rows = c.cnt[t.e], whole = rows & ~15, base = c.off[t.e];
+                if (rows != whole) {
+                    const uint32_t s = nt & 1u, bar = smem_u32(&c.tail_full[s]), at = tails + s * kTailBytes;
+                    if (!mbar_wait(smem_u32(&c.tail_empty[s]), ((nt >> 1) & 1u) ^ 1u, &c.dead)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_expect_tx(bar, kTailBytes);
+                    for (int b = 0; b < 2; ++b) {
+                        tma_load(at + b * kTailBlock, &atail, bar, m0 + b * 64, base + whole);
+                        tma_load(at + (2 + b) * kTailBlock, &btail, bar, n0 + b * 64, base + whole);
+                    }
+                    ++nt;
+                }
+                for (int r = 0; r < whole; r += kKB, ++it) {
                     const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
                     if (!mbar_wait(smem_u32(&c.empty[s]), ph ^ 1u, &c.dead)) {
                         ok = false;
                         break;
                     }
-                    const bool tail = rows - r < kKB && (rows & 15) != 0;
-                    const uint32_t bar = tail ? smem_u32(&c.tail[s]) : in_cta(smem_u32(&c.full[s]), 0);
+                    const uint32_t bar = in_cta(smem_u32(&c.full[s]), 0);
                     const uint32_t sa = ring + s * kStageBytes, sb = sa + kABytes;
-                    if (tail)
-                        mbar_expect_tx(bar, kStageBytes);
-                    else if (rank == 0)
-                        mbar_expect_tx(smem_u32(&c.full[s]), 2 * kStageBytes);
-                    else
-                        mbar_arrive_relaxed(bar);
+                    if (rank == 0) mbar_expect_tx(smem_u32(&c.full[s]), 2 * kStageBytes);
                     for (int b = 0; b < 2; ++b) {
                         tma_load(sa + b * kBlock, &amap, bar, m0 + b * 64, base + r);
                         tma_load(sb + b * kBlock, &bmap, bar, n0 + b * 64, base + r);
                     }
                 }
             }
-            if (!ok) drain_copies(c, rank == 0 ? it : 0, a.err);
+            if (!ok) {
+                drain_copies(c, rank == 0 ? it : 0, a.err);
+                volatile int go_on = 0;
+                for (uint32_t j = nt < 2 ? 0 : nt - 2; j < nt; ++j)
+                    mbar_wait(smem_u32(&c.tail_full[j & 1u]), (j >> 1) & 1u, &go_on);
+            }
         }
     } else if (warp == 1) {
         if (rank == 0 && elect_one()) {
-            uint32_t it = 0, tile = 0;
+            uint32_t it = 0, nt = 0, tile = 0;
             bool ok = true;
             const uint32_t idesc = tc_idesc(2 * kTileM, kTileN, 1, 1);
             for (GradTile t(a, first, step); t.valid() && ok; t.next()) {
-                const int rows = c.cnt[t.e];
+                const int rows = c.cnt[t.e], whole = rows & ~15;
                 if (rows == 0) continue;
                 const uint32_t acc = tile & 1u;
                 if (!mbar_wait(smem_u32(&c.acc_empty[acc]), ((tile >> 1) & 1u) ^ 1u, &c.dead)) {
@@ -622,21 +643,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
                 }
                 tc_fence_after();
                 const uint32_t d = c.tmem + acc * kTileN;
-                for (int r = 0; r < rows; r += kKB, ++it) {
+                for (int r = 0; r < whole; r += kKB, ++it) {
                     const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
-                    const int steps = (min(rows - r, kKB) + 15) / 16;
-                    // the last block may have been written by the clearing warps
-                    if (!(rows - r <= kKB ? mbar_wait<true>(smem_u32(&c.full[s]), ph, &c.dead)
-                                          : mbar_wait(smem_u32(&c.full[s]), ph, &c.dead))) {
+                    if (!mbar_wait(smem_u32(&c.full[s]), ph, &c.dead)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint32_t sa = ring + s * kStageBytes, sb = sa + kABytes;
+                    const int steps = min(whole - r, kKB) / 16;
                     for (int k = 0; k < steps; ++k)
                         tc_mma(d, tc_desc(sa + k * 2048, kBlock), tc_desc(sb + k * 2048, kBlock), idesc,
                                (r | k) != 0);
                     tc_commit(smem_u32(&c.empty[s]));
+                }
+                if (ok && rows != whole) {
+                    const uint32_t s = nt & 1u, at = tails + s * kTailBytes;
+                    ok = mbar_wait<true>(smem_u32(&c.tail_ready[s]), (nt >> 1) & 1u, &c.dead);
+                    if (!ok) break;
+                    tc_fence_after();
+                    tc_mma(d, tc_desc(at, kTailBlock), tc_desc(at + 2 * kTailBlock, kTailBlock), idesc, whole != 0);
+                    tc_commit(smem_u32(&c.tail_empty[s]));
+                    ++nt;
                 }
                 if (ok) tc_commit(smem_u32(&c.acc_full[acc]));
                 ++tile;
@@ -644,30 +672,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
             if (!ok) drain_products(c, a.err);
         }
     } else if (warp == 2 + kEpiWarps) {
-        // clears rows left .. 16 steps of every 64-feature block (the swizzle
-        // moves 16-byte units within a row's 128 bytes only)
-        uint32_t it = 0, phases = 0;  // phases: bit s, the phase of stage s's tail blocks
-        const uint32_t lane = threadIdx.x & 31;
+        // clears rows of the last steps (the swizzle moves 16-byte units within a
+        // row's 128 bytes only)
+        uint32_t nt = 0;
+        const int lane = threadIdx.x & 31;
         for (GradTile t(a, first, step); t.valid(); t.next()) {
-            const int rows = c.cnt[t.e], blocks = (rows + kKB - 1) / kKB;
-            it += blocks;
-            if ((rows & 15) == 0) continue;
-            const uint32_t s = (it - 1) % STAGES, sa = ring + s * kStageBytes;
-            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&c.tail[s]), (phases >> s) & 1u, &c.dead))) {
+            const int left = c.cnt[t.e] & 15;
+            if (left == 0) continue;
+            const uint32_t s = nt & 1u, at = tails + s * kTailBytes;
+            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&c.tail_full[s]), (nt >> 1) & 1u, &c.dead))) {
                 if (lane == 0) give_up(&c.dead, a.err);
                 break;
             }
-            phases ^= 1u << s;
-            const int left = rows - (blocks - 1) * kKB, units = (((left + 15) & ~15) - left) * 8;
-            for (int b = 0; b < kStageBytes / kBlock; ++b)
-                for (int x = (int)lane; x < units; x += 32) sts128(sa + b * kBlock + left * 128 + x * 16, 0, 0, 0, 0);
+            for (int b = 0; b < 4; ++b)
+                for (int x = left * 8 + lane; x < 16 * 8; x += 32) sts128(at + b * kTailBlock + x * 16, 0, 0, 0, 0);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(in_cta(smem_u32(&c.full[s]), 0));
+            if (lane == 0) mbar_arrive_cluster(in_cta(smem_u32(&c.tail_ready[s]), 0));
+            ++nt;
         }
     } else {
         const int lane = threadIdx.x & 31, quarter = warp & 3, side = (warp - 2) >> 2;
-        const uint32_t piece = ring + STAGES * kStageBytes + (warp - 2) * kPiece;
+        const uint32_t piece = tails + 2 * kTailBytes + (warp - 2) * kPiece;
         constexpr int kCols = F32 ? 32 : 64;
         uint32_t tile = 0;
         for (GradTile t(a, first, step); t.valid(); t.next()) {
@@ -791,12 +817,14 @@ cudaError_t launch_rows_product(int epi, const void* rows_in, int64_t nrows, con
 cudaError_t launch_weight_grad(const void* arows, const void* brows, int64_t nrows, int f32, GradArgs a,
                                int sm_count, cudaStream_t s)
 {
-    CUtensorMap amap, bmap;
-    const uint32_t box[2] = {64, kKB};
+    CUtensorMap amap, bmap, atail, btail;
+    const uint32_t box[2] = {64, kKB}, step[2] = {64, 16};
     const uint64_t ad[2] = {(uint64_t)a.M, (uint64_t)nrows}, as[1] = {(uint64_t)a.M * 2};
     const uint64_t bd[2] = {(uint64_t)a.N, (uint64_t)nrows}, bs[1] = {(uint64_t)a.N * 2};
     cudaError_t e = encode_tiles(&amap, arows, 2, ad, as, box);
     if (e == cudaSuccess) e = encode_tiles(&bmap, brows, 2, bd, bs, box);
+    if (e == cudaSuccess) e = encode_tiles(&atail, arows, 2, ad, as, step);
+    if (e == cudaSuccess) e = encode_tiles(&btail, brows, 2, bd, bs, step);
     if (e != cudaSuccess) return e;
     CUtensorMap dmap;
     const uint64_t es = f32 ? 4 : 2;
@@ -809,9 +837,11 @@ cudaError_t launch_weight_grad(const void* arows, const void* brows, int64_t nro
     a.nt = (a.N + kTileN - 1) / kTileN;
     const int64_t total = (int64_t)a.mt * a.nt * a.E;
     if (total > INT32_MAX) return cudaErrorInvalidValue;  // tiles are counted in 32 bits
-    constexpr int smem = 1024 + kGradStages * kStageBytes + kEpiWarps * kPiece;
-    return f32 ? launch_pairs(grad_kernel<true>, kGradThreads, smem, total, sm_count, s, amap, bmap, dmap, a)
-               : launch_pairs(grad_kernel<false>, kGradThreads, smem, total, sm_count, s, amap, bmap, dmap, a);
+    constexpr int smem = 1024 + kGradStages * kStageBytes + 2 * kTailBytes + kEpiWarps * kPiece;
+    return f32 ? launch_pairs(grad_kernel<true>, kGradThreads, smem, total, sm_count, s, amap, bmap, atail, btail,
+                                dmap, a)
+               : launch_pairs(grad_kernel<false>, kGradThreads, smem, total, sm_count, s, amap, bmap, atail, btail,
+                                dmap, a);
 }
 
 cudaError_t encode_tiles(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
