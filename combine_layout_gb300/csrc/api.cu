@@ -1213,13 +1213,13 @@ int moe_ep_norm_residual(moe_ep_group_t g, const void* o, const void* res, const
         return MOE_EP_ERR_INVALID;
     a.res_out = (uint4*)res_out;
     a.y = (uint4*)y;
-    return cuda_status(launch_norm(a, num_tokens, (cudaStream_t)stream));
+    return cuda_status(launch_norm(a, num_tokens, g->sm_count, (cudaStream_t)stream));
 }
 
 int moe_ep_norm_work_floats(moe_ep_group_t g, int64_t* floats)
 {
     if (!g || !floats) return MOE_EP_ERR_INVALID;
-    *floats = (int64_t)g->sm_count * norm_ctas(g->H) * 2 * g->H;
+    *floats = (int64_t)g->sm_count * 2 * g->H;
     return MOE_EP_OK;
 }
 

@@ -378,6 +378,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t rank = cluster_rank();
     const uint32_t ring = (smem_u32(dyn) + 1023u) & ~1023u;
 
+    if (threadIdx.x == 0) tma_prefetch_map(&wmap);
+    if (threadIdx.x < kRowBoxes) tma_prefetch_map(&rmap.box[threadIdx.x]);
+    griddep_launch_dependents();  // the next kernel's prologue runs under this one's end
     start_pair(c, warp);
     griddep_wait();
     tile_prefix(c, a, kTileN);
@@ -578,6 +581,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
     const int warp = threadIdx.x >> 5;
     const uint32_t rank = cluster_rank();
     const uint32_t ring = (smem_u32(dyn) + 1023u) & ~1023u;
+    if (threadIdx.x == 0) {
+        tma_prefetch_map(&amap);
+        tma_prefetch_map(&bmap);
+        tma_prefetch_map(&atail);
+        tma_prefetch_map(&btail);
+    }
+    griddep_launch_dependents();  // the next kernel's prologue runs under this one's end
     start_pair(c, warp);
     griddep_wait();
     tile_prefix(c, a, kTileN);

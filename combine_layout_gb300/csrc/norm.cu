@@ -85,24 +85,6 @@ __device__ __forceinline__ Vec vec_of(const float* p)
     return r;
 }
 
-__device__ __forceinline__ void unpack8(float (&f)[8], const uint4& v)
-{
-    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(u[i] << 16);
-        f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    }
-}
-
-__device__ __forceinline__ void load8(float (&f)[8], const float* __restrict__ p)
-{
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-    const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-}
-
 // Sums of N values over the CTA, in a fixed order; `part` is the caller's own
 // [N][32] piece of shared memory, not in use by another sum since the last
 // barrier.  One barrier.
@@ -127,236 +109,107 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float (*part)[32])
         for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
 }
 
-// Forward: one CTA per token, its row in registers (VPT vectors per thread);
-// the weights come from L1.  Rows are independent, so what hides the two sums'
-// latency is more CTAs per SM.
-template <int VPT>
-__global__ void __launch_bounds__(256, VPT <= 4 ? 4 : 2) norm_kernel(const NormArgs a)
-{
-    griddep_wait();
-    __shared__ float part[2][1][32];
-    const int nvec = a.H / 8, nt = blockDim.x;
-    const size_t t = blockIdx.x;
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    uint4 o[VPT];
-    Vec r[VPT];
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int v = threadIdx.x + i * nt;
-        o[i] = a.o && v < nvec ? __ldcs(a.o + t * nvec + v) : zero;
-    }
-    uint4 res[VPT];
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int v = threadIdx.x + i * nt;
-        res[i] = a.res && v < nvec ? __ldcs(a.res + t * nvec + v) : zero;
-    }
-    const f2 inv = pack(a.inv_h, a.inv_h), sc = pack(a.scale, a.scale);
-    float gt = a.gate && a.per_token ? __ldg(a.gate + t) : 1.f;
-    if (a.w_post) {
-        f2 s2 = pack(0.f, 0.f);
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const Vec x = widen(o[i]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) s2 = fma2(mul2(x.v[j], inv), x.v[j], s2);
-        }
-        float ss[1] = {sum2(s2)};
-        block_sum<1>(ss, part[0]);
-        gt *= rsqrtf(ss[0] + a.eps);
-    }
-    const f2 gg = pack(gt, gt);  // the token's gate times rstd(o)
-    f2 s2 = pack(0.f, 0.f);
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int v = threadIdx.x + i * nt;
-        if (v >= nvec) continue;
-        Vec u = widen(o[i]);
-        const Vec x = widen(res[i]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) u.v[j] = mul2(u.v[j], gg);
-        if (a.w_post) {
-            const Vec w = vec_of(a.w_post + v * 8);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) u.v[j] = mul2(u.v[j], w.v[j]);
-        }
-        if (a.gate && !a.per_token) {
-            const Vec w = vec_of(a.gate + v * 8);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) u.v[j] = mul2(u.v[j], w.v[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            r[i].v[j] = fma2(sc, x.v[j], u.v[j]);
-            s2 = fma2(mul2(r[i].v[j], inv), r[i].v[j], s2);
-        }
-        if (a.res_out) a.res_out[t * nvec + v] = narrow(r[i]);
-    }
-    if (!a.y) return;
-    float ss[1] = {sum2(s2)};
-    block_sum<1>(ss, part[1]);
-    const float q = rsqrtf(ss[0] + a.eps);
-    const f2 qq = pack(q, q);
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int v = threadIdx.x + i * nt;
-        if (v >= nvec) continue;
-        const Vec w = vec_of(a.w_pre + v * 8);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) r[i].v[j] = mul2(w.v[j], mul2(r[i].v[j], qq));
-        a.y[t * nvec + v] = narrow(r[i]);
-    }
-}
+// Forward: a CTA takes tokens in grid-stride order, a token's row in registers
+// (VPT vectors per thread), and loads the next token's row as soon as this one's
+// has been combined into r, so loads are in flight through both sums' latency.
+// The weights come from L1.
+constexpr int norm_resident(int vpt) { return vpt <= 2 ? 4 : vpt == 4 ? 3 : 1; }  // CTAs per SM
 
-// Backward, rows wider than the pipelined form below takes: persistent CTAs
-// take tokens in grid-stride order; a thread keeps its columns' gradients in registers over all the CTA's tokens and
-// writes them to the CTA's row of the workspace, which norm_columns_kernel
-// adds up in a fixed order (no atomics: the result does not depend on
-// scheduling).
 template <int VPT>
-__global__ void __launch_bounds__(1024, 1) norm_bwd_kernel(const NormBwdArgs b)
+__global__ void __launch_bounds__(256, norm_resident(VPT)) norm_kernel(const NormArgs a, int T)
 {
     griddep_wait();
-    __shared__ float part[5][2][32];
-    const NormArgs& a = b.f;
+    __shared__ float part[2][2][1][32];
     const int nvec = a.H / 8, nt = blockDim.x;
-    float c_pre[VPT][8] = {}, c_dm[VPT][8] = {};
-    for (int t = blockIdx.x; t < b.T; t += gridDim.x) {
+    const f2 inv = pack(a.inv_h, a.inv_h), sc = pack(a.scale, a.scale);
+    uint4 o[VPT], res[VPT];
+    auto load = [&](int t) {
         const size_t base = (size_t)t * nvec;
-        float o[VPT][8], u[VPT][8], r[VPT][8], d[VPT][8];
         const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int v = threadIdx.x + i * nt;
-            unpack8(o[i], a.o && v < nvec ? __ldcs(a.o + base + v) : zero);
-            unpack8(r[i], a.res && v < nvec ? __ldcs(a.res + base + v) : zero);
-            unpack8(d[i], b.dr && v < nvec ? __ldcs(b.dr + base + v) : zero);
+            o[i] = a.o && v < nvec ? __ldcs(a.o + base + v) : zero;
         }
-        float p = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = threadIdx.x + i * nt;
+            res[i] = a.res && v < nvec ? __ldcs(a.res + base + v) : zero;
+        }
+    };
+    int t = blockIdx.x;
+    if (t < T) load(t);
+    for (int turn = 0; t < T; turn ^= 1, t += gridDim.x) {
+        const size_t base = (size_t)t * nvec;
+        float gt = a.gate && a.per_token ? __ldg(a.gate + t) : 1.f;
         if (a.w_post) {
-            float s[1] = {0.f};
+            f2 s2 = pack(0.f, 0.f);
 #pragma unroll
-            for (int i = 0; i < VPT; ++i)
+            for (int i = 0; i < VPT; ++i) {
+                const Vec x = widen(o[i]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) s[0] = fmaf(o[i][j] * a.inv_h, o[i][j], s[0]);
-            block_sum<1>(s, part[0]);
-            p = rsqrtf(s[0] + a.eps);
+                for (int j = 0; j < 4; ++j) s2 = fma2(mul2(x.v[j], inv), x.v[j], s2);
+            }
+            float ss[1] = {sum2(s2)};
+            block_sum<1>(ss, part[turn][0]);
+            gt *= rsqrtf(ss[0] + a.eps);
         }
-        const float gt = a.gate && a.per_token ? __ldg(a.gate + t) : 1.f;
-        float s2[2] = {0.f, 0.f};
-        float dy[VPT][8];
+        const f2 gg = pack(gt, gt);  // the token's gate times rstd(o)
+        Vec r[VPT];
+        f2 s2 = pack(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int v = threadIdx.x + i * nt;
-            float w[8], g[8];
-            unpack8(dy[i], b.dy && v < nvec ? __ldcs(b.dy + base + v) : zero);
-            if (a.w_post && v < nvec) load8(w, a.w_post + v * 8);
-            if (a.gate && !a.per_token && v < nvec) load8(g, a.gate + v * 8);
+            Vec u = widen(o[i]);
+            const Vec x = widen(res[i]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                u[i][j] = a.w_post ? (v < nvec ? w[j] * (o[i][j] * p) : 0.f) : o[i][j];
-                const float gj = a.gate && !a.per_token ? (v < nvec ? g[j] : 0.f) : gt;
-                r[i][j] = fmaf(gj, u[i][j], a.scale * r[i][j]);
+            for (int j = 0; j < 4; ++j) u.v[j] = mul2(u.v[j], gg);
+            if (a.w_post && v < nvec) {
+                const Vec w = vec_of(a.w_post + v * 8);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) u.v[j] = mul2(u.v[j], w.v[j]);
             }
-            if (b.dy && v < nvec) {
-                load8(w, a.w_pre + v * 8);
+            if (a.gate && !a.per_token && v < nvec) {
+                const Vec w = vec_of(a.gate + v * 8);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    s2[0] = fmaf(r[i][j] * a.inv_h, r[i][j], s2[0]);
-                    s2[1] = fmaf(r[i][j], w[j] * dy[i][j], s2[1]);
-                }
+                for (int j = 0; j < 4; ++j) u.v[j] = mul2(u.v[j], w.v[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                r[i].v[j] = fma2(sc, x.v[j], u.v[j]);
+                s2 = fma2(mul2(r[i].v[j], inv), r[i].v[j], s2);
             }
         }
-        if (b.dy) {
-            block_sum<2>(s2, part[1]);
-            const float q = rsqrtf(s2[0] + a.eps);
-            const float k = s2[1] * q * a.inv_h;  // mean(v n)
+        const int next = t + gridDim.x;
+        if (next < T) load(next);
+        if (a.res_out)
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 const int v = threadIdx.x + i * nt;
-                if (v < nvec) {
-                    float w[8];
-                    load8(w, a.w_pre + v * 8);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float n = r[i][j] * q;
-                        c_pre[i][j] = fmaf(dy[i][j], n, c_pre[i][j]);
-                        d[i][j] = fmaf(q, w[j] * dy[i][j] - n * k, d[i][j]);
-                    }
-                }
+                if (v < nvec) a.res_out[base + v] = narrow(r[i]);
             }
-        }
-        // gradients of the gate and, with w_post, of the norm after the block
-        s2[0] = s2[1] = 0.f;
+        if (!a.y) continue;
+        float ss[1] = {sum2(s2)};
+        block_sum<1>(ss, part[turn][1]);
+        const float q = rsqrtf(ss[0] + a.eps);
+        const f2 qq = pack(q, q);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int v = threadIdx.x + i * nt;
-            if (v < nvec) {
-                if (b.dres) {
-                    float x[8];
+            if (v >= nvec) continue;
+            const Vec w = vec_of(a.w_pre + v * 8);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] = a.scale * d[i][j];
-                    b.dres[base + v] = pack8(x);
-                }
-                float w[8], g[8];
-                if (a.w_post) load8(w, a.w_post + v * 8);
-                if (a.gate && !a.per_token) load8(g, a.gate + v * 8);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float m = a.w_post ? o[i][j] * p : o[i][j];
-                    s2[0] = fmaf(d[i][j], u[i][j], s2[0]);
-                    c_dm[i][j] = fmaf(gt * d[i][j], m, c_dm[i][j]);
-                    d[i][j] *= a.gate && !a.per_token ? g[j] : gt;
-                    if (a.w_post) {
-                        d[i][j] *= w[j];
-                        s2[1] = fmaf(d[i][j], m, s2[1]);
-                    }
-                }
-            }
-        }
-        const bool token_gate = b.dgate && a.per_token;
-        if (a.w_post || token_gate) {
-            block_sum<2>(s2, part[3]);
-            if (token_gate && threadIdx.x == 0) b.dgate[t] = s2[0];
-        }
-        if (b.d_o) {
-            const float k = s2[1] * a.inv_h;
-#pragma unroll
-            for (int i = 0; i < VPT; ++i) {
-                const int v = threadIdx.x + i * nt;
-                if (v < nvec) {
-                    if (a.w_post)
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) d[i][j] = p * (d[i][j] - (o[i][j] * p) * k);
-                    b.d_o[base + v] = pack8(d[i]);
-                }
-            }
-        }
-        __syncthreads();  // the sums' shared memory before the next token
-    }
-    float* row = b.work + (size_t)blockIdx.x * 2 * a.H;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int v = threadIdx.x + i * nt;
-        if (v < nvec) {
-#pragma unroll
-            for (int j = 0; j < 8; j += 4) {
-                *reinterpret_cast<float4*>(row + v * 8 + j) =
-                    make_float4(c_pre[i][j], c_pre[i][j + 1], c_pre[i][j + 2], c_pre[i][j + 3]);
-                *reinterpret_cast<float4*>(row + a.H + v * 8 + j) =
-                    make_float4(c_dm[i][j], c_dm[i][j + 1], c_dm[i][j + 2], c_dm[i][j + 3]);
-            }
+            for (int j = 0; j < 4; ++j) r[i].v[j] = mul2(w.v[j], mul2(r[i].v[j], qq));
+            a.y[base + v] = narrow(r[i]);
         }
     }
 }
 
-// ---------------------------------------------------------------------------
-// Sums of 8 values over the CTA in a fixed order, every thread getting all;
-// one barrier.  In a warp the values are halved at each step (4 + 2 + 1 + 1 +
-// 1 exchanges instead of 40); part is [2][8][32], used in turn.
-__device__ __forceinline__ void block_sum8(float (&v)[8], float (*part)[32])
+// Sums of 8 values over a warp: lane l gets the sum of value l / 4.  The values
+// are halved at each step (4 + 2 + 1 + 1 + 1 exchanges instead of 40).
+__device__ __forceinline__ float warp_sum8(float (&v)[8])
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int n = 4, o = 16; n >= 1; n >>= 1, o >>= 1) {
         const bool hi = (lane & o) != 0;
@@ -368,16 +221,7 @@ __device__ __forceinline__ void block_sum8(float (&v)[8], float (*part)[32])
     }
     v[0] += __shfl_xor_sync(0xffffffffu, v[0], 2);
     v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
-    // lane holds value (lane >> 4) * 4 + ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1) = lane >> 2
-    if ((lane & 3) == 0) part[lane >> 2][warp] = v[0];
-    __syncthreads();
-    float x = 0.f;
-    const int which = lane >> 2;
-    for (int i = lane & 3; i < nw; i += 4) x += part[which][i];
-    x += __shfl_xor_sync(0xffffffffu, x, 2);
-    x += __shfl_xor_sync(0xffffffffu, x, 1);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __shfl_sync(0xffffffffu, x, i * 4);
+    return v[0];
 }
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar)
@@ -387,62 +231,76 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  : "memory");
 }
 
-// Backward, pipelined (H <= 8192).  Persistent CTAs take tokens in grid-stride
-// order, a thread owning two vectors of 8 columns; one thread copies the rows
-// of the tokens ahead into a ring in shared memory (cp.async.bulk).
+// Backward, rows of 2048 to 8192 channels.  Persistent CTAs take tokens in
+// grid-stride order; their rows are copied ahead into a ring in shared memory
+// (cp.async.bulk), three tokens deep.
 //
 // All sums over a token's row follow from r, v = w_pre dy and u once rstd(o) is
 // known:  sum D u = sum u dr + q sum u v - q^2 k sum u r   (q = rstd(r), k =
 // mean(v n)), and mean(z m) is that sum over H (with the gate), so no sum needs
-// the gradient D itself.  That leaves one barrier per token, between which a
-// thread works on three tokens: the outputs of token i, the sums of token i + 1
-// and mean(o^2) of token i + 2.
+// the gradient D itself.  Half of the warps take the sums of one token after the
+// other (with mean(o^2) of the token after), the other half the outputs of the
+// tokens whose sums are done; a thread has two vectors of 8 columns (one up to H =
+// 4096, where two would leave half of the warps out).  16384 x 7168: 279 us, 5.1
+// TB/s; what bounds it is the time an output warp takes for its share of a row
+// (2.5 us), at 72 registers a thread.  With one set of warps doing both in turn
+// the SM's issue slots were less than half used (336 us).
 //
 // The gradients of w_post and of the channel gate are both column sums of D m
 // (times the other weight), so two column accumulators serve all three; they
 // stay in registers and end in the CTA's row of the workspace, which
-// norm_columns_kernel adds up in a fixed order (no atomics: the result does not
-// depend on scheduling).
-constexpr int kRowVecs = 2;       // vectors of a thread
-constexpr int kRowThreads = 512;  // at most
-constexpr int kRows = 3;          // tokens in the ring
-constexpr int kNormSmem = 227 * 1024 - 2560;  // dynamic shared memory of a CTA, less the static part
+// norm_columns_kernel adds up in a fixed order (no atomics on them: the result
+// does not depend on scheduling).
+constexpr int kRows = 3;     // tokens in the ring
+constexpr int kNormSmem = 227 * 1024 - 2048;  // dynamic shared memory of a CTA, less the static part
 
-template <bool WS>
-__global__ void __launch_bounds__(kRowThreads, 1) norm_bwd_rows_kernel(const NormBwdArgs b)
+// What the outputs of a token need.
+struct RowStats {
+    float p, gt, q, kq, kz;  // rstd(o), the token's gate, q, -k q, -mean(z m)
+};
+
+// WS: the weights fit into shared memory beside the ring (H <= 7168); TOKEN: a
+// gate per token.
+template <int kRowVecs, bool WS, bool TOKEN>
+__global__ void __launch_bounds__(kRowVecs == 2 && WS ? 896 : 1024, 1) norm_bwd_rows_kernel(const NormBwdArgs b)
 {
     const NormArgs& a = b.f;
     extern __shared__ __align__(16) uint8_t dyn[];
-    __shared__ float part[2][8][32];
-    __shared__ uint64_t bar_o[kRows], bar_r[kRows];
+    __shared__ float part[2][8][16];
+    __shared__ uint64_t bar_o[kRows], bar_r[kRows], bar_s[kRows];  // o, the other rows, the sums
+    __shared__ RowStats stats[kRows];
+    __shared__ unsigned done[kRows];  // output warps that are through with the ring's rows
     __shared__ volatile int dead;
-    const int H = a.H, nvec = H / 8, nt = blockDim.x;
+    // the first half of the threads takes the sums, the second the outputs
+    const int H = a.H, nvec = H / 8, nt = blockDim.x / 2, lane = threadIdx.x & 31;
+    const bool summing = (int)threadIdx.x < nt;
+    const int tid = summing ? threadIdx.x : threadIdx.x - nt, warp = tid >> 5, warps = nt >> 5;
     const uint32_t rb = (uint32_t)H * 2;
-    uint4* ring = reinterpret_cast<uint4*>(dyn);                  // [kRows][4][nvec]: o, res, dr, dy
+    uint4* ring = reinterpret_cast<uint4*>(dyn);                    // [kRows][4][nvec]: o, res, dr, dy
     float* sw = reinterpret_cast<float*>(ring + kRows * 4 * nvec);  // [2][H]: w_post gate, w_pre
-    const bool chan = a.gate && !a.per_token, post = a.w_post != nullptr;
+    const bool chan = !TOKEN && a.gate, post = a.w_post != nullptr;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kRows; ++i) {
             mbar_init(smem_u32(&bar_o[i]), 1);
             mbar_init(smem_u32(&bar_r[i]), 1);
+            mbar_init(smem_u32(&bar_s[i]), 1);
+            done[i] = 0;
         }
         dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    griddep_wait();
     // inputs that are absent read as zero
     if (!a.o || !a.res || !b.dr || !b.dy)
-        for (int v = threadIdx.x; v < kRows * 4 * nvec; v += nt) ring[v] = make_uint4(0u, 0u, 0u, 0u);
+        for (int v = threadIdx.x; v < kRows * 4 * nvec; v += 2 * nt) ring[v] = make_uint4(0u, 0u, 0u, 0u);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
+    griddep_wait();
 
     const int first = blockIdx.x, step = gridDim.x;
     const int count = first < b.T ? (b.T - first + step - 1) / step : 0;
-    int issued = 0;  // thread 0: tokens whose copies were started
     auto load = [&](int i) {  // the CTA's i-th token
         if (i >= count) return;
-        issued = i + 1;
         const size_t at = (size_t)(first + i * step) * nvec;
         uint4* d = ring + (i % kRows) * 4 * nvec;
         uint32_t bar = smem_u32(&bar_o[i % kRows]);
@@ -473,166 +331,412 @@ __global__ void __launch_bounds__(kRowThreads, 1) norm_bwd_rows_kernel(const Nor
         }
         return w;
     };
-    if (WS) {
-        // a thread stages the columns that it alone reads: no barrier
-#pragma unroll
-        for (int x = 0; x < kRowVecs; ++x) {
-            const int v = threadIdx.x + x * nt;
-            if (v >= nvec) continue;
-#pragma unroll
-            for (int which = 0; which < 2; ++which) {
-                const Vec w = fetch(which, v);
-                ulonglong2* d = reinterpret_cast<ulonglong2*>(sw + which * H + v * 8);
-                d[0] = make_ulonglong2(w.v[0], w.v[1]);
-                d[1] = make_ulonglong2(w.v[2], w.v[3]);
-            }
+    if (WS)
+        for (int x = threadIdx.x; x < 2 * nvec; x += 2 * nt) {
+            // in two planes, so that neighbouring threads' 16 bytes are neighbours
+            const int which = x >= nvec, v = x - which * nvec;
+            const Vec w = fetch(which, v);
+            ulonglong2* d = reinterpret_cast<ulonglong2*>(sw + which * H) + v;
+            d[0] = make_ulonglong2(w.v[0], w.v[1]);
+            d[nvec] = make_ulonglong2(w.v[2], w.v[3]);
         }
-    }
-    auto weight = [&](int which, int v) { return WS ? vec_of(sw + which * H + v * 8) : fetch(which, v); };
+    __syncthreads();
+    auto weight = [&](int which, int v) {
+        if (!WS) return fetch(which, v);
+        const ulonglong2* d = reinterpret_cast<const ulonglong2*>(sw + which * H) + v;
+        const ulonglong2 x = d[0], y = d[nvec];
+        Vec w;
+        w.v[0] = x.x; w.v[1] = x.y; w.v[2] = y.x; w.v[3] = y.y;
+        return w;
+    };
 
-    Vec c_pre[kRowVecs], c_dm[kRowVecs];
-#pragma unroll
-    for (int x = 0; x < kRowVecs; ++x)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) c_pre[x].v[j] = c_dm[x].v[j] = pack(0.f, 0.f);
     const f2 inv = pack(a.inv_h, a.inv_h), sc = pack(a.scale, a.scale);
-
-    // Bounded waits for a token's rows; every thread waits for itself, and a
-    // thread that gives up takes the whole CTA with it at the next barrier.
+    // Bounded waits; a thread that gives up sets `dead`, which ends the others'.
     auto wait = [&](uint64_t* bars, int i) {
-        if (!mbar_wait(smem_u32(&bars[i % kRows]), (i / kRows) & 1, &dead)) dead = 1;
-    };
-    auto token_gate = [&](int i) { return a.gate && a.per_token ? __ldg(a.gate + first + i * step) : 1.f; };
-    // s[5] = this thread's part of mean(o^2) of token i
-    auto mean_o = [&](int i, float (&s)[8]) {
-        if (i >= count || !a.o) return;
-        wait(bar_o, i);
-        if (!post) return;
-        f2 acc = pack(0.f, 0.f);
-#pragma unroll
-        for (int x = 0; x < kRowVecs; ++x) {
-            const int v = threadIdx.x + x * nt;
-            if (v >= nvec) continue;
-            const Vec o = widen(ring[(i % kRows) * 4 * nvec + v]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc = fma2(mul2(o.v[j], inv), o.v[j], acc);
-        }
-        s[5] = sum2(acc);
-    };
-    // mean(r^2), mean(r v), and the sums of u (times the channel gate) with dr, v and r of token i
-    auto sums = [&](int i, float p, float gt, float (&s)[8]) {
-        if (i >= count) return;
-        wait(bar_r, i);
-        const uint4* row = ring + (i % kRows) * 4 * nvec;
-        const f2 pp = pack(p, p), gg = pack(gt, gt);
-        f2 s0 = pack(0.f, 0.f), s1 = s0, s2 = s0, s3 = s0, s4 = s0;
-#pragma unroll
-        for (int x = 0; x < kRowVecs; ++x) {
-            const int v = threadIdx.x + x * nt;
-            if (v >= nvec) continue;
-            const Vec o = widen(row[v]), res = widen(row[nvec + v]), dr = widen(row[2 * nvec + v]),
-                      dy = widen(row[3 * nvec + v]);
-            const Vec wg = weight(0, v), wq = weight(1, v);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const f2 u = mul2(wg.v[j], mul2(o.v[j], pp));
-                const f2 r = fma2(sc, res.v[j], mul2(u, gg));
-                const f2 vv = mul2(wq.v[j], dy.v[j]), ri = mul2(r, inv);
-                s0 = fma2(ri, r, s0);
-                s1 = fma2(ri, vv, s1);
-                s2 = fma2(u, dr.v[j], s2);
-                s3 = fma2(u, vv, s3);
-                s4 = fma2(u, r, s4);
-            }
-        }
-        s[0] = sum2(s0);
-        s[1] = sum2(s1);
-        s[2] = sum2(s2);
-        s[3] = sum2(s3);
-        s[4] = sum2(s4);
-    };
-    // the outputs of token i from its sums
-    auto outputs = [&](int i, float p, float gt, const float (&s)[8]) {
-        const size_t base = (size_t)(first + i * step) * nvec;
-        const uint4* row = ring + (i % kRows) * 4 * nvec;
-        const float q = b.dy ? rsqrtf(s[0] + a.eps) : 0.f;
-        const float k = s[1] * q;                                    // mean(v n)
-        const float du = s[2] + q * s[3] - q * q * k * s[4];         // sum of D u
-        if (b.dgate && threadIdx.x == 0) b.dgate[first + i * step] = du;
-        const float kz = du * gt * a.inv_h;                          // mean(z m)
-        const f2 pp = pack(p, p), gg = pack(gt, gt), qq = pack(q, q), kq = pack(-k * q, -k * q), nz = pack(-kz, -kz);
-#pragma unroll
-        for (int x = 0; x < kRowVecs; ++x) {
-            const int v = threadIdx.x + x * nt;
-            if (v >= nvec) continue;
-            const Vec o = widen(row[v]), res = widen(row[nvec + v]), dr = widen(row[2 * nvec + v]),
-                      dy = widen(row[3 * nvec + v]);
-            const Vec wg = weight(0, v), wq = weight(1, v);
-            Vec ds, dz;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const f2 m = mul2(o.v[j], pp);
-                const f2 r = fma2(sc, res.v[j], mul2(mul2(wg.v[j], m), gg));
-                const f2 n = mul2(r, qq);
-                c_pre[x].v[j] = fma2(dy.v[j], n, c_pre[x].v[j]);
-                f2 d = fma2(mul2(wq.v[j], dy.v[j]), qq, dr.v[j]);
-                d = fma2(n, kq, d);
-                ds.v[j] = mul2(sc, d);
-                d = mul2(d, gg);
-                c_dm[x].v[j] = fma2(d, m, c_dm[x].v[j]);
-                dz.v[j] = mul2(wg.v[j], d);
-                if (post) dz.v[j] = mul2(pp, fma2(m, nz, dz.v[j]));
-            }
-            if (b.dres) b.dres[base + v] = narrow(ds);
-            if (b.d_o) b.d_o[base + v] = narrow(dz);
-        }
+        const bool ok = mbar_wait(smem_u32(&bars[i % kRows]), (i / kRows) & 1, &dead);
+        if (!ok) dead = 1;
+        return ok;
     };
 
-    float s[8] = {};
-    mean_o(0, s);
-    block_sum8(s, part[0]);
-    float p = post ? rsqrtf(s[5] + a.eps) : 1.f, gt = count > 0 ? token_gate(0) : 1.f;
-    float st[8] = {};  // sums of the token whose outputs come next
-    sums(0, p, gt, st);
-    mean_o(1, st);
-    st[6] = (float)dead;
-    block_sum8(st, part[1]);
-    float p1 = post ? rsqrtf(st[5] + a.eps) : 1.f;
-    for (int i = 0; i < count && st[6] == 0.f; ++i) {
-        float nx[8] = {};
-        const float gt1 = i + 1 < count ? token_gate(i + 1) : 1.f;
-        sums(i + 1, p1, gt1, nx);
-        outputs(i, p, gt, st);
-        mean_o(i + 2, nx);
-        nx[6] = (float)dead;
-        block_sum8(nx, part[i & 1]);
-        // every thread is done with token i: its place in the ring is free
-        if (threadIdx.x == 0) load(i + kRows);
-        p = p1;
-        gt = gt1;
-        p1 = post ? rsqrtf(nx[5] + a.eps) : 1.f;
+    if (summing) {
+        // a warp's sums to shared memory, then a barrier of these warps; whether
+        // one of their threads has given up
+        auto exchange = [&](float (&s)[8], int turn) {
+            const float x = warp_sum8(s);
+            if ((lane & 3) == 0) part[turn][lane >> 2][warp] = x;
+            uint32_t gone;
+            asm volatile(
+                "{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbar.red.or.pred q, 1, %2, p;\nselp.b32 %0, 1, 0, q;\n}"
+                : "=r"(gone)
+                : "r"((uint32_t)dead), "r"(nt)
+                : "memory");
+            return gone != 0;
+        };
+        // the sum of value `which` over the warps
+        auto total = [&](int which, int turn) {
+            float x = lane < warps ? part[turn][which][lane] : 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) st[j] = nx[j];
-    }
-    if (st[6] != 0.f) {
-        if (threadIdx.x == 0) {
-            *(volatile unsigned*)(b.err + kErrTimeout) = 1u;
-            // copies still in flight land in this CTA's shared memory
-            volatile int go_on = 0;
-            for (int i = max(0, issued - kRows); i < issued; ++i) {
-                if (a.o) mbar_wait(smem_u32(&bar_o[i % kRows]), (i / kRows) & 1, &go_on);
-                mbar_wait(smem_u32(&bar_r[i % kRows]), (i / kRows) & 1, &go_on);
+            for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o, 16);
+            return __shfl_sync(0xffffffffu, x, 0);
+        };
+        // s[5] = this thread's part of mean(o^2) of token i
+        auto mean_o = [&](int i, float (&s)[8]) {
+            if (i >= count || !a.o) return;
+            wait(bar_o, i);
+            if (!post) return;
+            f2 acc = pack(0.f, 0.f);
+#pragma unroll
+            for (int x = 0; x < kRowVecs; ++x) {
+                const int v = tid + x * nt;
+                if (v >= nvec) continue;
+                const Vec o = widen(ring[(i % kRows) * 4 * nvec + v]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc = fma2(mul2(o.v[j], inv), o.v[j], acc);
             }
+            s[5] = sum2(acc);
+        };
+        float s[8] = {};
+        mean_o(0, s);
+        bool gone = exchange(s, 1);
+        float p = post && count > 0 ? rsqrtf(total(5, 1) + a.eps) : 1.f;
+        for (int i = 0; i < count && !gone; ++i) {
+            const int turn = i & 1;
+            wait(bar_r, i);
+            const float gt = TOKEN ? __ldg(a.gate + first + i * step) : 1.f;
+            const uint4* row = ring + (i % kRows) * 4 * nvec;
+            const f2 pp = pack(p, p), gg = pack(gt, gt);
+            f2 s0 = pack(0.f, 0.f), s1 = s0, s2 = s0, s3 = s0, s4 = s0;
+            // mean(r^2), mean(r v), and the sums of u (times the channel gate) with dr, v and r
+#pragma unroll
+            for (int x = 0; x < kRowVecs; ++x) {
+                const int v = tid + x * nt;
+                if (v >= nvec) continue;
+                const Vec o = widen(row[v]), res = widen(row[nvec + v]), dr = widen(row[2 * nvec + v]),
+                          dy = widen(row[3 * nvec + v]);
+                const Vec wg = weight(0, v), wq = weight(1, v);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const f2 u = mul2(wg.v[j], mul2(o.v[j], pp));
+                    const f2 r = fma2(sc, res.v[j], TOKEN ? mul2(u, gg) : u);
+                    const f2 vv = mul2(wq.v[j], dy.v[j]), ri = mul2(r, inv);
+                    s0 = fma2(ri, r, s0);
+                    s1 = fma2(ri, vv, s1);
+                    s2 = fma2(u, dr.v[j], s2);
+                    s3 = fma2(u, vv, s3);
+                    s4 = fma2(u, r, s4);
+                }
+            }
+            float t[8] = {sum2(s0), sum2(s1), sum2(s2), sum2(s3), sum2(s4), 0.f, 0.f, 0.f};
+            mean_o(i + 1, t);
+            gone = exchange(t, turn);
+            if (gone) break;
+            if (warp == 0) {
+                const float q = b.dy ? rsqrtf(total(0, turn) + a.eps) : 0.f;
+                const float k = total(1, turn) * q;                                               // mean(v n)
+                const float du = total(2, turn) + q * total(3, turn) - q * q * k * total(4, turn);  // sum of D u
+                if (lane == 0) {
+                    if (TOKEN && b.dgate) b.dgate[first + i * step] = du;
+                    stats[i % kRows] = RowStats{p, gt, q, -k * q, post ? -du * gt * a.inv_h : 0.f};
+                    mbar_arrive(smem_u32(&bar_s[i % kRows]));
+                }
+            }
+            p = post ? rsqrtf(total(5, turn) + a.eps) : 1.f;
+        }
+    } else {
+        Vec c_pre[kRowVecs], c_dm[kRowVecs];
+#pragma unroll
+        for (int x = 0; x < kRowVecs; ++x)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) c_pre[x].v[j] = c_dm[x].v[j] = pack(0.f, 0.f);
+        for (int i = 0; i < count; ++i) {
+            if (!__all_sync(0xffffffffu, wait(bar_s, i))) break;
+            // the copies of this token, which the sums have waited for
+            wait(bar_r, i);
+            if (a.o) wait(bar_o, i);
+            const RowStats st = stats[i % kRows];
+            const size_t base = (size_t)(first + i * step) * nvec;
+            const uint4* row = ring + (i % kRows) * 4 * nvec;
+            const f2 pp = pack(st.p, st.p), gg = pack(st.gt, st.gt), qq = pack(st.q, st.q), kq = pack(st.kq, st.kq),
+                     nz = pack(st.kz, st.kz);
+#pragma unroll
+            for (int x = 0; x < kRowVecs; ++x) {
+                const int v = tid + x * nt;
+                if (v >= nvec) continue;
+                const Vec o = widen(row[v]), res = widen(row[nvec + v]), dr = widen(row[2 * nvec + v]),
+                          dy = widen(row[3 * nvec + v]);
+                const Vec wg = weight(0, v), wq = weight(1, v);
+                Vec ds, dz;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const f2 m = mul2(o.v[j], pp), u = mul2(wg.v[j], m);
+                    const f2 n = mul2(fma2(sc, res.v[j], TOKEN ? mul2(u, gg) : u), qq);
+                    c_pre[x].v[j] = fma2(dy.v[j], n, c_pre[x].v[j]);
+                    f2 d = fma2(mul2(wq.v[j], dy.v[j]), qq, dr.v[j]);
+                    d = fma2(n, kq, d);
+                    ds.v[j] = mul2(sc, d);
+                    if (TOKEN) d = mul2(d, gg);
+                    c_dm[x].v[j] = fma2(d, m, c_dm[x].v[j]);
+                    dz.v[j] = mul2(wg.v[j], d);
+                    if (post) dz.v[j] = mul2(pp, fma2(m, nz, dz.v[j]));
+                }
+                if (b.dres) b.dres[base + v] = narrow(ds);
+                if (b.d_o) b.d_o[base + v] = narrow(dz);
+            }
+            // the last warp through with the token's place in the ring fills it again
+            __syncwarp();
+            if (lane == 0) {
+                __threadfence_block();
+                if (atomicAdd(&done[i % kRows], 1u) == (unsigned)warps - 1u) {
+                    done[i % kRows] = 0;
+                    __threadfence_block();
+                    load(i + kRows);
+                }
+            }
+        }
+        float* row = b.work + (size_t)blockIdx.x * 2 * H;
+#pragma unroll
+        for (int x = 0; x < kRowVecs; ++x) {
+            const int v = tid + x * nt;
+            if (v >= nvec) continue;
+            ulonglong2* d0 = reinterpret_cast<ulonglong2*>(row + v * 8);
+            ulonglong2* d1 = reinterpret_cast<ulonglong2*>(row + H + v * 8);
+            d0[0] = make_ulonglong2(c_pre[x].v[0], c_pre[x].v[1]);
+            d0[1] = make_ulonglong2(c_pre[x].v[2], c_pre[x].v[3]);
+            d1[0] = make_ulonglong2(c_dm[x].v[0], c_dm[x].v[1]);
+            d1[1] = make_ulonglong2(c_dm[x].v[2], c_dm[x].v[3]);
+        }
+    }
+    __syncthreads();
+    if (dead) {
+        if (threadIdx.x == 0) *(volatile unsigned*)(b.err + kErrTimeout) = 1u;
+        // copies still in flight land in this CTA's shared memory: every barrier's
+        // current phase is given its time
+        volatile int go_on = 0;
+        if (threadIdx.x < 2 * kRows) {
+            uint64_t* bar = threadIdx.x < kRows ? &bar_o[threadIdx.x] : &bar_r[threadIdx.x - kRows];
+            for (uint32_t ph = 0; ph < 2; ++ph) mbar_wait(smem_u32(bar), ph, &go_on);
         }
         __syncthreads();
     }
-    float* row = b.work + (size_t)blockIdx.x * 2 * H;
+}
+
+// Backward, narrower and wider rows: the same sums and outputs (see
+// norm_bwd_rows_kernel), with a CTA taking a contiguous range of tokens, `most`
+// at a time, in three passes: mean(o^2), the other sums -- both with the 16 warps
+// spread over the batch's rows -- and then the outputs, with a thread on the same
+// vectors of every row.  Narrow rows need few threads each, so the sums of many
+// rows share a barrier (16384 x 1024: 72 us, 81 with a barrier per row); rows
+// wider than 8192 do not fit the ring.  At 4096 x 7168 the later passes' reads
+// from L2 are what it waits for (129 us).
+constexpr int kMaxBatch = 16;  // tokens at a time: one warp to a row at least
+constexpr int kBwdThreads = 512;
+constexpr int kBwdWarps = kBwdThreads / 32;
+
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
+template <int VPT>
+__global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_kernel(const NormBwdArgs b, int most, int groups)
+{
+    const NormArgs& a = b.f;
+    extern __shared__ __align__(16) uint8_t dyn[];
+    __shared__ float part[kBwdWarps][8];
+    __shared__ RowStats stats[kMaxBatch];
+    float* sw = reinterpret_cast<float*>(dyn);  // [2][H]: w_post gate (channel), w_pre; later the groups' sums
+    const int H = a.H, nvec = H / 8, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const bool chan = a.gate && !a.per_token, post = a.w_post != nullptr;
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    griddep_wait();
+
+    const int first = (int)((int64_t)b.T * blockIdx.x / gridDim.x);
+    const int last = (int)((int64_t)b.T * (blockIdx.x + 1) / gridDim.x);
+    int batch = most;  // a power of two; with fewer tokens, more warps to each row
+    while (batch > 1 && batch / 2 >= last - first) batch /= 2;
+    const int wpr = kBwdWarps / batch;  // warps to a row
+    auto prefetch = [&](int t) {
+        const int n = min(batch, last - t);
+        if (n <= 0) return;
+        const size_t at = (size_t)t * nvec;
+        const uint32_t bytes = (uint32_t)n * H * 2;
+        if (a.o) prefetch_l2(a.o + at, bytes);
+        if (a.res) prefetch_l2(a.res + at, bytes);
+        if (b.dr) prefetch_l2(b.dr + at, bytes);
+        if (b.dy) prefetch_l2(b.dy + at, bytes);
+    };
+    if (tid == 0) prefetch(first);
+    for (int v = tid; v < nvec; v += kBwdThreads)
 #pragma unroll
-    for (int x = 0; x < kRowVecs; ++x) {
-        const int v = threadIdx.x + x * nt;
+        for (int j = 0; j < 8; j += 4) {
+            const int c = v * 8 + j;
+            float4 w = make_float4(1.f, 1.f, 1.f, 1.f), x = w;
+            if (post) w = __ldg(reinterpret_cast<const float4*>(a.w_post + c));
+            if (chan) {
+                const float4 g = __ldg(reinterpret_cast<const float4*>(a.gate + c));
+                w = make_float4(w.x * g.x, w.y * g.y, w.z * g.z, w.w * g.w);
+            }
+            if (a.w_pre) x = __ldg(reinterpret_cast<const float4*>(a.w_pre + c));
+            *reinterpret_cast<float4*>(sw + c) = w;
+            *reinterpret_cast<float4*>(sw + H + c) = x;
+        }
+
+    // pass 3's share: group `grp` of threads takes every groups-th row
+    const int width = kBwdThreads / groups, grp = tid / width, col = tid - grp * width;
+    Vec c_pre[VPT], c_dm[VPT];
+#pragma unroll
+    for (int x = 0; x < VPT; ++x)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c_pre[x].v[j] = c_dm[x].v[j] = pack(0.f, 0.f);
+    const f2 inv = pack(a.inv_h, a.inv_h), sc = pack(a.scale, a.scale);
+    __syncthreads();
+
+    for (int t0 = first; t0 < last; t0 += batch) {
+        if (tid == 0) prefetch(t0 + batch);
+        const int n = min(batch, last - t0);
+        const int row = warp / wpr, piece = warp - row * wpr;  // passes 1 and 2: this warp's row and part of it
+        const bool mine = row < n;
+        const size_t base = (size_t)(t0 + (mine ? row : 0)) * nvec;
+        float p = 1.f;
+        if (post) {
+            if (mine) {
+                f2 acc = pack(0.f, 0.f);
+#pragma unroll 4
+                for (int v = piece * 32 + lane; v < nvec; v += wpr * 32) {
+                    const Vec o = widen(a.o[base + v]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc = fma2(mul2(o.v[j], inv), o.v[j], acc);
+                }
+                float s = sum2(acc);
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                if (lane == 0) part[warp][5] = s;
+            }
+            __syncthreads();
+            if (mine) {
+                float s = 0.f;
+                for (int i = 0; i < wpr; ++i) s += part[row * wpr + i][5];
+                p = rsqrtf(s + a.eps);
+            }
+        }
+        const float gt = a.gate && a.per_token && mine ? __ldg(a.gate + t0 + row) : 1.f;
+        if (mine) {
+            // mean(r^2), mean(r v), and the sums of u (times the channel gate) with dr, v and r
+            const f2 pp = pack(p, p), gg = pack(gt, gt);
+            f2 s0 = pack(0.f, 0.f), s1 = s0, s2 = s0, s3 = s0, s4 = s0;
+#pragma unroll 2
+            for (int v = piece * 32 + lane; v < nvec; v += wpr * 32) {
+                const Vec o = widen(a.o ? a.o[base + v] : zero), res = widen(a.res ? a.res[base + v] : zero),
+                          dr = widen(b.dr ? b.dr[base + v] : zero), dy = widen(b.dy ? b.dy[base + v] : zero);
+                const Vec wg = vec_of(sw + v * 8), wq = vec_of(sw + H + v * 8);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const f2 u = mul2(wg.v[j], mul2(o.v[j], pp));
+                    const f2 r = fma2(sc, res.v[j], mul2(u, gg));
+                    const f2 vv = mul2(wq.v[j], dy.v[j]), ri = mul2(r, inv);
+                    s0 = fma2(ri, r, s0);
+                    s1 = fma2(ri, vv, s1);
+                    s2 = fma2(u, dr.v[j], s2);
+                    s3 = fma2(u, vv, s3);
+                    s4 = fma2(u, r, s4);
+                }
+            }
+            float s[8] = {sum2(s0), sum2(s1), sum2(s2), sum2(s3), sum2(s4), 0.f, 0.f, 0.f};
+            const float x = warp_sum8(s);
+            if ((lane & 3) == 0 && lane < 20) part[warp][lane >> 2] = x;
+        }
+        __syncthreads();
+        if (mine && piece == 0 && lane == 0) {
+            float s[5] = {};
+            for (int i = 0; i < wpr; ++i)
+#pragma unroll
+                for (int j = 0; j < 5; ++j) s[j] += part[warp + i][j];
+            const float q = b.dy ? rsqrtf(s[0] + a.eps) : 0.f;
+            const float k = s[1] * q;                             // mean(v n)
+            const float du = s[2] + q * s[3] - q * q * k * s[4];  // sum of D u
+            if (b.dgate) b.dgate[t0 + row] = du;
+            stats[row] = RowStats{p, gt, q, -k * q, post ? -du * gt * a.inv_h : 0.f};
+        }
+        __syncthreads();
+        // the outputs, each row's next loads in flight under the current ones
+        uint4 in[VPT][4];
+        auto load = [&](int i) {
+            const size_t at = (size_t)(t0 + i) * nvec;
+#pragma unroll
+            for (int x = 0; x < VPT; ++x) {
+                const int v = col + x * width;
+                const bool ok = v < nvec;
+                in[x][0] = ok && a.o ? a.o[at + v] : zero;
+                in[x][1] = ok && a.res ? a.res[at + v] : zero;
+                in[x][2] = ok && b.dr ? b.dr[at + v] : zero;
+                in[x][3] = ok && b.dy ? b.dy[at + v] : zero;
+            }
+        };
+        if (grp < n && grp < groups) load(grp);
+        for (int i = grp; i < n && grp < groups; i += groups) {
+            const RowStats st = stats[i];
+            const size_t at = (size_t)(t0 + i) * nvec;
+            const f2 pp = pack(st.p, st.p), gg = pack(st.gt, st.gt), qq = pack(st.q, st.q), kq = pack(st.kq, st.kq),
+                     nz = pack(st.kz, st.kz);
+            uint4 cur[VPT][4];
+#pragma unroll
+            for (int x = 0; x < VPT; ++x)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) cur[x][j] = in[x][j];
+            if (i + groups < n) load(i + groups);
+#pragma unroll
+            for (int x = 0; x < VPT; ++x) {
+                const int v = col + x * width;
+                if (v >= nvec) continue;
+                const Vec o = widen(cur[x][0]), res = widen(cur[x][1]), dr = widen(cur[x][2]), dy = widen(cur[x][3]);
+                const Vec wg = vec_of(sw + v * 8), wq = vec_of(sw + H + v * 8);
+                Vec ds, dz;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const f2 m = mul2(o.v[j], pp);
+                    const f2 n = mul2(fma2(sc, res.v[j], mul2(mul2(wg.v[j], m), gg)), qq);
+                    c_pre[x].v[j] = fma2(dy.v[j], n, c_pre[x].v[j]);
+                    f2 d = fma2(mul2(wq.v[j], dy.v[j]), qq, dr.v[j]);
+                    d = fma2(n, kq, d);
+                    ds.v[j] = mul2(sc, d);
+                    d = mul2(d, gg);
+                    c_dm[x].v[j] = fma2(d, m, c_dm[x].v[j]);
+                    dz.v[j] = mul2(pp, fma2(m, nz, mul2(wg.v[j], d)));
+                }
+                if (b.dres) b.dres[at + v] = narrow(ds);
+                if (b.d_o) b.d_o[at + v] = narrow(dz);
+            }
+        }
+    }
+
+    // the groups' column sums, added in order, into the CTA's row of the workspace
+    if (groups > 1) {
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < VPT; ++x) {
+            const int v = col + x * width;
+            if (v < nvec && grp < groups)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    *reinterpret_cast<f2*>(sw + (size_t)(2 * grp) * H + v * 8 + 2 * j) = c_pre[x].v[j];
+                    *reinterpret_cast<f2*>(sw + (size_t)(2 * grp + 1) * H + v * 8 + 2 * j) = c_dm[x].v[j];
+                }
+        }
+        __syncthreads();
+        for (int c = tid; c < 2 * H; c += kBwdThreads) {
+            float s = 0.f;
+            for (int g = 0; g < groups; ++g) s += sw[(size_t)g * 2 * H + c];
+            b.work[(size_t)blockIdx.x * 2 * H + c] = s;
+        }
+        return;
+    }
+    float* out = b.work + (size_t)blockIdx.x * 2 * H;
+#pragma unroll
+    for (int x = 0; x < VPT; ++x) {
+        const int v = col + x * width;
         if (v >= nvec) continue;
-        ulonglong2* d0 = reinterpret_cast<ulonglong2*>(row + v * 8);
-        ulonglong2* d1 = reinterpret_cast<ulonglong2*>(row + H + v * 8);
+        ulonglong2* d0 = reinterpret_cast<ulonglong2*>(out + v * 8);
+        ulonglong2* d1 = reinterpret_cast<ulonglong2*>(out + H + v * 8);
         d0[0] = make_ulonglong2(c_pre[x].v[0], c_pre[x].v[1]);
         d0[1] = make_ulonglong2(c_pre[x].v[2], c_pre[x].v[3]);
         d1[0] = make_ulonglong2(c_dm[x].v[0], c_dm[x].v[1]);
@@ -641,29 +745,39 @@ __global__ void __launch_bounds__(kRowThreads, 1) norm_bwd_rows_kernel(const Nor
 }
 
 // Adds up the CTAs' column sums: dw_pre, and from the sums of D m the gradients
-// of w_post (times the channel gate) and of the channel gate (times w_post).
-__global__ void __launch_bounds__(256) norm_columns_kernel(const float* __restrict__ work, int rows, int H,
-                                                           const float* w_post, const float* gate, float* dw_pre,
-                                                           float* dw_post, float* dgate)
+// of w_post (times the channel gate) and of the channel gate (times w_post).  A
+// CTA takes 128 of the 2 H columns, its 16 warps every 16th row with all loads in
+// flight; they are added in a fixed order.
+constexpr int kColWarps = 16;
+
+__global__ void __launch_bounds__(kColWarps * 32) norm_columns_kernel(const float* __restrict__ work, int rows,
+                                                                      int H, const float* w_post, const float* gate,
+                                                                      float* dw_pre, float* dw_post, float* dgate)
 {
     griddep_wait();
-    if (blockIdx.y == 0 ? !dw_pre : !dw_post && !dgate) return;
-    __shared__ float s[8][32];
-    const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + lane;
-    float v = 0.f;
-    if (c < H)
-        for (int i = part; i < rows; i += 8) v += work[((size_t)i * 2 + blockIdx.y) * H + c];
-    s[part][lane] = v;
+    __shared__ float s[kColWarps][128];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int c = blockIdx.x * 128 + lane * 4;  // H is a multiple of 8: four columns stay in one half
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (c < 2 * H)
+#pragma unroll 10
+        for (int i = warp; i < rows; i += kColWarps) {
+            const float4 x = *reinterpret_cast<const float4*>(work + (size_t)i * 2 * H + c);
+            v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+        }
+    *reinterpret_cast<float4*>(&s[warp][lane * 4]) = v;
     __syncthreads();
-    if (part != 0 || c >= H) return;
+    const int col = blockIdx.x * 128 + threadIdx.x;
+    if (threadIdx.x >= 128 || col >= 2 * H) return;
+    float x = 0.f;
 #pragma unroll
-    for (int i = 1; i < 8; ++i) v += s[i][lane];
-    if (blockIdx.y == 0) {
-        dw_pre[c] = v;
+    for (int i = 0; i < kColWarps; ++i) x += s[i][threadIdx.x];
+    if (col < H) {
+        if (dw_pre) dw_pre[col] = x;
     } else {
-        if (dw_post) dw_post[c] = gate ? v * __ldg(gate + c) : v;
-        if (dgate) dgate[c] = w_post ? v * __ldg(w_post + c) : v;
+        const int h = col - H;
+        if (dw_post) dw_post[h] = gate ? x * __ldg(gate + h) : x;
+        if (dgate) dgate[h] = w_post ? x * __ldg(w_post + h) : x;
     }
 }
 
@@ -677,40 +791,60 @@ cudaError_t launch_smem(void (*k)(KArgs...), int grid, int threads, int smem, cu
 
 }  // namespace
 
-cudaError_t launch_norm(const NormArgs& a, int T, cudaStream_t s)
+cudaError_t launch_norm(const NormArgs& a, int T, int sm_count, cudaStream_t s)
 {
     if (T <= 0) return cudaSuccess;
     const int nvec = a.H / 8;
     const int vpt = nvec <= 256 ? 1 : nvec <= 512 ? 2 : nvec <= 1024 ? 4 : 8;
     const int threads = ((nvec + vpt - 1) / vpt + 31) & ~31;
-    if (vpt == 1) return launch_pdl(norm_kernel<1>, dim3(T), dim3(threads), s, a);
-    if (vpt == 2) return launch_pdl(norm_kernel<2>, dim3(T), dim3(threads), s, a);
-    if (vpt == 4) return launch_pdl(norm_kernel<4>, dim3(T), dim3(threads), s, a);
-    return launch_pdl(norm_kernel<8>, dim3(T), dim3(threads), s, a);
+    // narrow rows: as many threads per SM as with wide ones
+    const int ctas = norm_resident(vpt) * (threads >= 128 ? 1 : 128 / threads) * sm_count;
+    const dim3 grid(T < ctas ? T : ctas), block(threads);
+    if (vpt == 1) return launch_pdl(norm_kernel<1>, grid, block, s, a, T);
+    if (vpt == 2) return launch_pdl(norm_kernel<2>, grid, block, s, a, T);
+    if (vpt == 4) return launch_pdl(norm_kernel<4>, grid, block, s, a, T);
+    return launch_pdl(norm_kernel<8>, grid, block, s, a, T);
 }
 
 cudaError_t launch_norm_bwd(const NormBwdArgs& b, float* dw_pre, float* dw_post, float* dgate_channel,
                             int sm_count, cudaStream_t s)
 {
     const int H = b.f.H, nvec = H / 8;
-    const int most = sm_count * norm_ctas(H), grid = b.T < most ? b.T : most;
+    const int grid = b.T < sm_count ? b.T : sm_count;
     if (grid > 0) {
-        const int ring = kRows * 4 * 2 * H, weights = 8 * H;
         cudaError_t e;
-        if (nvec <= kRowVecs * kRowThreads) {
-            const int threads = ((nvec + kRowVecs - 1) / kRowVecs + 31) & ~31;
-            const bool ws = ring + weights <= kNormSmem;
-            e = ws ? launch_smem(norm_bwd_rows_kernel<true>, grid, threads, ring + weights, s, b)
-                   : launch_smem(norm_bwd_rows_kernel<false>, grid, threads, ring, s, b);
+        const bool token = b.f.gate && b.f.per_token;
+        if (H >= 2048 && H <= 8192) {
+            const int ring = kRows * 4 * 2 * H, weights = 8 * H;
+            const int vecs = H <= 4096 ? 1 : 2;
+            const int threads = 2 * (((nvec + vecs - 1) / vecs + 31) & ~31);
+            const bool ws = ring + weights <= kNormSmem;  // always up to 4096
+#define MOEEP_NORM_BWD(V, W, K) launch_smem(norm_bwd_rows_kernel<V, W, K>, grid, threads, ring + (W ? weights : 0), s, b)
+            if (vecs == 1)
+                e = token ? MOEEP_NORM_BWD(1, true, true) : MOEEP_NORM_BWD(1, true, false);
+            else if (ws)
+                e = token ? MOEEP_NORM_BWD(2, true, true) : MOEEP_NORM_BWD(2, true, false);
+            else
+                e = token ? MOEEP_NORM_BWD(2, false, true) : MOEEP_NORM_BWD(2, false, false);
+#undef MOEEP_NORM_BWD
         } else {
-            const int threads = ((nvec + 1) / 2 + 31) & ~31;
-            e = launch_pdl(norm_bwd_kernel<2>, dim3(grid), dim3(threads), s, b);
+            // two vectors a thread (four for the widest rows), and as many groups
+            // of threads as fit
+            const int vpt = nvec <= 2 * kBwdThreads ? 2 : 4;
+            const int width = ((nvec + vpt - 1) / vpt + 31) & ~31;
+            int groups = 1;
+            // a batch's rows are about 130 KB at most: narrow rows come more at a time
+            const int batch = H > 8192 ? 4 : kMaxBatch;
+            while (groups < batch && groups * 2 * width <= kBwdThreads) groups *= 2;
+            const int smem = 8 * H * groups;
+            e = vpt == 2 ? launch_smem(norm_bwd_kernel<2>, grid, kBwdThreads, smem, s, b, batch, groups)
+                         : launch_smem(norm_bwd_kernel<4>, grid, kBwdThreads, smem, s, b, batch, groups);
         }
         if (e != cudaSuccess) return e;
     }
     if (!dw_pre && !dw_post && !dgate_channel) return cudaSuccess;
     const float* gate = b.f.per_token ? nullptr : b.f.gate;
-    return launch_pdl(norm_columns_kernel, dim3((H + 31) / 32, 2), dim3(256), s, (const float*)b.work, grid, H,
+    return launch_pdl(norm_columns_kernel, dim3((2 * H + 127) / 128), dim3(kColWarps * 32), s, (const float*)b.work, grid, H,
                       b.f.w_post, gate, dw_pre, dw_post, dgate_channel);
 }
 

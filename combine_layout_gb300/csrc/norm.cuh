@@ -6,11 +6,8 @@
 
 namespace moeep {
 
-// Widest row the norms take: two vectors of 8 for each of 1024 threads.
+// Widest row the norms take: four vectors of 8 for each of 512 threads.
 constexpr int kMaxNormWidth = 16384;
-
-// CTAs per SM of the persistent kernels: narrow rows need few threads each.
-inline int norm_ctas(int H) { return H >= 4096 ? 1 : H >= 2048 ? 2 : H >= 1024 ? 4 : 8; }
 
 struct NormArgs {
     const uint4* o;       // bf16 [T][H] (may be null)
@@ -23,7 +20,7 @@ struct NormArgs {
     int H, per_token;
     float scale, eps, inv_h;
 };
-cudaError_t launch_norm(const NormArgs& a, int T, cudaStream_t s);
+cudaError_t launch_norm(const NormArgs& a, int T, int sm_count, cudaStream_t s);
 
 struct NormBwdArgs {
     NormArgs f;        // the forward pass's inputs

@@ -46,6 +46,11 @@ __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes)
                  : "memory");
 }
 
+__device__ __forceinline__ void mbar_arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 // Pairs of CTAs (clusters of two): the rank in the pair, a shared-memory
 // address in CTA `rank`, an arrival on a barrier given by such an address, and
 // a barrier over the pair.
