@@ -1,0 +1,98 @@
+"""One mixture-of-experts block on an EpPipeline: norm, route, dispatch, the
+experts' gated feed-forward, combine, and the norm after the block fused with
+its gate, the residual and the next block's norm -- and the backward pass of all
+of it.  Allocation and argument marshalling only, like ``pipeline``: every step
+runs in libmoeep's kernels; the router's product is the caller's (``scores``).
+
+    h           [T][H] residual stream, bf16
+    x         = norm(h; w_in)
+    topk, w   = route(scores(x))
+    rows      = dispatch(x);  hid = act(Wg rows) * (Wu rows);  y = Wd hid
+    o         = combine(y, w)
+    h'        = res_scale h + gate norm(o; w_post)
+    x_next    = norm(h'; w_next)
+"""
+from __future__ import annotations
+
+import torch
+
+from . import moe_ep as ep
+from .pipeline import EpPipeline
+
+
+class MoeBlock:
+    """Weights: w_gate_up [E][2F][H] and w_down [E][H][F] bf16; w_in, w_post (or
+    None), w_next [H] and gate ([H], [T] with gate_per_token, or None) fp32.
+    The pipeline is a bf16 one; with ``training`` the forward pass keeps what
+    ``backward`` needs."""
+
+    def __init__(self, pipe: EpPipeline, w_gate_up, w_down, w_in, w_post, w_next, gate=None,
+                 gate_per_token: bool = False, res_scale: float = 1.0, act: int = ep.MOE_EP_ACT_SILU,
+                 eps: float = 1e-6, training: bool = False):
+        if pipe.fp8:
+            raise ValueError("MoeBlock takes a bf16 pipeline (moe_ep_dequant serves FP8 rows)")
+        self.p, self.act, self.eps, self.training = pipe, act, eps, training
+        self.w_gate_up, self.w_down = w_gate_up, w_down
+        self.w_in, self.w_post, self.w_next = w_in, w_post, w_next
+        self.gate, self.gate_per_token, self.res_scale = gate, gate_per_token, res_scale
+        F, dev = w_down.shape[2], pipe.device
+        rows = lambda n: torch.empty((pipe.rows, n), dtype=torch.bfloat16, device=dev)  # noqa: E731
+        tokens = lambda: torch.empty((pipe.S, pipe.H), dtype=torch.bfloat16, device=dev)  # noqa: E731
+        self.hid, self.y = rows(F), rows(pipe.H)
+        self.x, self.h_out, self.x_next = tokens(), tokens(), tokens()
+        self.gate_up = None
+        if training:
+            self.gate_up, self.d_gate_up, self.d_rows = rows(2 * F), rows(2 * F), rows(pipe.H)
+            self.d_o, self.d_h, self.d_x = tokens(), tokens(), tokens()
+            self.ones = torch.ones((pipe.S, pipe.k), dtype=torch.float32, device=dev)
+            f32 = lambda t: None if t is None else torch.zeros_like(t)  # noqa: E731
+            self.d_topk_w = torch.empty((pipe.S, pipe.k), dtype=torch.float32, device=dev)
+            self.dw_gate_up = torch.zeros(w_gate_up.shape, dtype=torch.float32, device=dev)
+            self.dw_down = torch.zeros(w_down.shape, dtype=torch.float32, device=dev)
+            self.dw_in, self.dw_post, self.dw_next, self.dgate = f32(w_in), f32(w_post), f32(w_next), f32(gate)
+            self.work = torch.empty(ep.moe_ep_norm_work_floats(pipe.group), dtype=torch.float32, device=dev)
+
+    def forward(self, h, scores, num_groups: int = 1, topk_groups: int = 1,
+                weight_mode: int = ep.MOE_EP_W_SCORE_NORM, stream=None):
+        """h [T][H] -> (h', x_next).  scores: x -> fp32 [T][E], on ``stream``."""
+        p, T = self.p, h.shape[0]
+        self.h, x = h, self.x[:T]
+        ep.moe_ep_norm_residual(p.group, None, h, None, None, self.w_in, None, x, eps=self.eps, stream=stream)
+        p.route(scores(x), T, num_groups, topk_groups, 0, weight_mode, stream)
+        p.dispatch(x, stream)
+        ep.moe_ep_ffn_gate_up(p.handle, p.recv_x, self.w_gate_up, self.hid, self.gate_up, self.act, stream=stream)
+        ep.moe_ep_ffn_down(p.handle, self.hid, self.w_down, self.y, stream=stream)
+        self.o = p.combine(self.y, stream=stream)
+        ep.moe_ep_norm_residual(p.group, self.o, h, self.w_post, self.gate, self.w_next, self.h_out[:T],
+                                self.x_next[:T], self.res_scale, self.gate_per_token, self.eps, stream=stream)
+        return self.h_out[:T], self.x_next[:T]
+
+    def backward(self, d_h_out, d_x_next, d_x_router=None, accumulate: bool = False, stream=None):
+        """Gradients of (h', x_next) -> the gradient of h; those of the weights
+        are left in dw_* and dgate, that of the gate weights in d_topk_w.  The
+        experts' weight gradients are fp32 and, with ``accumulate``, added up
+        over calls.  d_x_router(d_topk_w) gives the router's share of x's
+        gradient, bf16 [T][H], or None when the router is not trained."""
+        if not self.training:
+            raise ValueError("the block was not made for training")
+        p, T = self.p, self.h.shape[0]
+        d_o, d_h, d_x = self.d_o[:T], self.d_h[:T], self.d_x[:T]
+        ep.moe_ep_norm_residual_backward(p.group, self.o, self.h, self.w_post, self.gate, self.w_next, d_h_out,
+                                         d_x_next, d_o, d_h, self.dw_post, self.dgate, self.dw_next, self.work,
+                                         self.res_scale, self.gate_per_token, self.eps, stream=stream)
+        # the rows' gradients in, the rows of x's gradient out of the same buffer
+        ep.moe_ep_combine_backward(p.handle, d_o, self.y, p.topk_w[:T], self.d_rows, self.d_topk_w[:T], stream=stream)
+        ep.moe_ep_ffn_down_backward(p.handle, self.d_rows, self.w_down, self.gate_up, self.d_gate_up, self.hid,
+                                    self.act, stream=stream)
+        ep.moe_ep_ffn_weight_grad(p.handle, self.d_rows, self.hid, self.dw_down, accumulate, stream=stream)
+        ep.moe_ep_ffn_weight_grad(p.handle, self.d_gate_up, p.recv_x, self.dw_gate_up, accumulate, stream=stream)
+        ep.moe_ep_ffn_gate_up_backward(p.handle, self.d_gate_up, self.w_gate_up, self.d_rows, stream=stream)
+        # the dispatch's backward: a token's rows added up
+        p.combine(self.d_rows, self.ones[:T], d_x, stream)
+        extra = d_x_router(self.d_topk_w[:T]) if d_x_router is not None else None
+        if extra is not None:
+            with torch.cuda.stream(stream or torch.cuda.current_stream(p.device)):
+                d_x += extra
+        ep.moe_ep_norm_residual_backward(p.group, None, self.h, None, None, self.w_in, d_h, d_x, None, d_h, None,
+                                         None, self.dw_in, self.work, eps=self.eps, stream=stream)
+        return d_h
