@@ -299,12 +299,21 @@ __device__ __forceinline__ void epi_down_bwd(const uint32_t (&r)[2][16], const R
 
 // Stages of the ring, and an epilogue warp's piece of shared memory: what is
 // left of 227 KB beside it.
-constexpr int rows_stages(int epi) { return epi == kRowsDownBwd ? 5 : 6; }
-constexpr int rows_stage_bytes(int epi) { return epi == kRowsDownBwd ? 6144 : epi == kRowsGateUp ? 3072 : 2048; }
-constexpr int kStageBytes = (kTileM + kTileN / 2) * kKB * 2;  // a CTA's 128 rows of each operand
-constexpr int rows_smem(int epi)
+// With few rows an expert (tiles of at most kFewN) the stages are smaller and more:
+// what bounds the kernel then is the weights in flight.
+constexpr int kFewN = 64;
+constexpr int kFewRows = 48;  // on average, at most: 64 experts x 7168 x 4096 with 8 rows each 549 -> 525 us,
+                              // 16 x 4096 x 2688 with 48 rows each 64.8 -> 61.7, with 64 the same, with 96 67.1 -> 71.8
+constexpr int rows_stages(int epi, int nt)
 {
-    return 1024 + rows_stages(epi) * kStageBytes + kEpiWarps * rows_stage_bytes(epi);
+    return nt == kFewN ? (epi == kRowsDownBwd ? 8 : 9) : (epi == kRowsDownBwd ? 5 : 6);
+}
+constexpr int rows_stage_bytes(int epi) { return epi == kRowsDownBwd ? 6144 : epi == kRowsGateUp ? 3072 : 2048; }
+constexpr int ring_bytes(int nt) { return (kTileM + nt / 2) * kKB * 2; }  // a CTA's share of a stage
+constexpr int kStageBytes = ring_bytes(kTileN);
+constexpr int rows_smem(int epi, int nt)
+{
+    return 1024 + rows_stages(epi, nt) * ring_bytes(nt) + kEpiWarps * rows_stage_bytes(epi);
 }
 
 // Barriers, tensor memory and the pair; every thread of both CTAs.
@@ -364,13 +373,13 @@ __device__ __forceinline__ void drain_products(Control<STAGES>& c, unsigned* err
     mbar_wait(smem_u32(&c.drain), 0, &go_on);
 }
 
-template <int EPI>
+template <int EPI, int NT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     rows_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ RowMaps rmap,
                 const RowsArgs a)
 {
     constexpr bool A_MN = EPI == kRowsDownBwd || EPI == kRowsStoreT;
-    constexpr int STAGES = rows_stages(EPI);
+    constexpr int STAGES = rows_stages(EPI, NT), kStageBytes = ring_bytes(NT);
     constexpr int kABytes = kTileM * kKB * 2;
     extern __shared__ uint8_t dyn[];
     __shared__ Control<STAGES> c;
@@ -383,7 +392,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     griddep_launch_dependents();  // the next kernel's prologue runs under this one's end
     start_pair(c, warp);
     griddep_wait();
-    tile_prefix(c, a, kTileN);
+    tile_prefix(c, a, NT);
     const int total = c.pre[a.E] * a.mt, first = blockIdx.x >> 1, step = gridDim.x >> 1;
     const int kblocks = (a.K + kKB - 1) / kKB;
 
@@ -436,7 +445,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     break;
                 }
                 tc_fence_after();
-                const uint32_t d = c.tmem + acc * kTileN;
+                const uint32_t d = c.tmem + acc * NT;
                 const uint32_t idesc = tc_idesc(2 * kTileM, t.n, A_MN, 0);
                 for (int kb = 0; kb < kblocks; ++kb, ++it) {
                     const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
@@ -476,7 +485,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 break;
             }
             tc_fence_after();
-            const uint32_t src = c.tmem + acc * kTileN + ((uint32_t)(quarter * 32) << 16);
+            const uint32_t src = c.tmem + acc * NT + ((uint32_t)(quarter * 32) << 16);
             const uint32_t release = in_cta(smem_u32(&c.acc_empty[acc]), 0);
             if (n0 >= t.n && lane == 0) mbar_arrive_relaxed(release);
             for (; n0 < t.n; n0 += 2 * kChunk) {
@@ -813,15 +822,23 @@ cudaError_t launch_rows_product(int epi, const void* rows_in, int64_t nrows, con
         if (e != cudaSuccess) return e;
     }
     a.mt = (int)(((epi == kRowsGateUp ? 2 * F : M) + 2 * kTileM - 1) / (2 * kTileM));
+    // few rows an expert on average: small tiles (an expert with more takes several)
+    const int nt = max_rows <= (int64_t)a.E * kFewRows ? kFewN : kTileN;
     // an upper bound of the tiles: every expert with rows ends in a partial tile
-    const int64_t bound = (int64_t)a.mt * ((max_rows < a.E ? max_rows : a.E) + max_rows / kTileN);
+    const int64_t bound = (int64_t)a.mt * ((max_rows < a.E ? max_rows : a.E) + max_rows / nt);
     if (bound > INT32_MAX) return cudaErrorInvalidValue;  // tiles are counted in 32 bits
+#define MOEEP_ROWS(EPI)                                                                                      \
+    return nt == kFewN ? launch_pairs(rows_kernel<EPI, kFewN>, kThreads, rows_smem(EPI, kFewN), bound,        \
+                                      sm_count, s, wmap, rmap, a)                                             \
+                       : launch_pairs(rows_kernel<EPI, kTileN>, kThreads, rows_smem(EPI, kTileN), bound,      \
+                                      sm_count, s, wmap, rmap, a)
     switch (epi) {
-        case kRowsGateUp: return launch_pairs(rows_kernel<kRowsGateUp>, kThreads, rows_smem(kRowsGateUp), bound, sm_count, s, wmap, rmap, a);
-        case kRowsStore: return launch_pairs(rows_kernel<kRowsStore>, kThreads, rows_smem(kRowsStore), bound, sm_count, s, wmap, rmap, a);
-        case kRowsDownBwd: return launch_pairs(rows_kernel<kRowsDownBwd>, kThreads, rows_smem(kRowsDownBwd), bound, sm_count, s, wmap, rmap, a);
-        default: return launch_pairs(rows_kernel<kRowsStoreT>, kThreads, rows_smem(kRowsStoreT), bound, sm_count, s, wmap, rmap, a);
+        case kRowsGateUp: MOEEP_ROWS(kRowsGateUp);
+        case kRowsStore: MOEEP_ROWS(kRowsStore);
+        case kRowsDownBwd: MOEEP_ROWS(kRowsDownBwd);
+        default: MOEEP_ROWS(kRowsStoreT);
     }
+#undef MOEEP_ROWS
 }
 
 cudaError_t launch_weight_grad(const void* arows, const void* brows, int64_t nrows, int f32, GradArgs a,
