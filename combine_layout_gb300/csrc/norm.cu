@@ -113,7 +113,7 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float (*part)[32])
 // (VPT vectors per thread), and loads the next token's row as soon as this one's
 // has been combined into r, so loads are in flight through both sums' latency.
 // The weights come from L1.
-constexpr int norm_resident(int vpt) { return vpt <= 2 ? 4 : vpt == 4 ? 3 : 1; }  // CTAs per SM
+constexpr int norm_resident(int vpt) { return vpt == 1 ? 5 : vpt == 2 ? 4 : vpt == 4 ? 3 : 1; }  // CTAs per SM
 
 template <int VPT>
 __global__ void __launch_bounds__(256, norm_resident(VPT)) norm_kernel(const NormArgs a, int T)
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(256, norm_resident(VPT)) norm_kernel(const Nor
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 const int v = threadIdx.x + i * nt;
-                if (v < nvec) a.res_out[base + v] = narrow(r[i]);
+                if (v < nvec) __stcs(a.res_out + base + v, narrow(r[i]));
             }
         if (!a.y) continue;
         float ss[1] = {sum2(s2)};
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(256, norm_resident(VPT)) norm_kernel(const Nor
             const Vec w = vec_of(a.w_pre + v * 8);
 #pragma unroll
             for (int j = 0; j < 4; ++j) r[i].v[j] = mul2(w.v[j], mul2(r[i].v[j], qq));
-            a.y[base + v] = narrow(r[i]);
+            __stcs(a.y + base + v, narrow(r[i]));
         }
     }
 }
@@ -231,7 +231,7 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  : "memory");
 }
 
-// Backward, rows of 2048 to 8192 channels.  Persistent CTAs take tokens in
+// Backward, rows of more than 2048 and up to 8192 channels.  Persistent CTAs take tokens in
 // grid-stride order; their rows are copied ahead into a ring in shared memory
 // (cp.async.bulk), three tokens deep.
 //
@@ -479,8 +479,8 @@ __global__ void __launch_bounds__(kRowVecs == 2 && WS ? 896 : 1024, 1) norm_bwd_
                     dz.v[j] = mul2(wg.v[j], d);
                     if (post) dz.v[j] = mul2(pp, fma2(m, nz, dz.v[j]));
                 }
-                if (b.dres) b.dres[base + v] = narrow(ds);
-                if (b.d_o) b.d_o[base + v] = narrow(dz);
+                if (b.dres) __stcs(b.dres + base + v, narrow(ds));
+                if (b.d_o) __stcs(b.d_o + base + v, narrow(dz));
             }
             // the last warp through with the token's place in the ring fills it again
             __syncwarp();
@@ -798,7 +798,9 @@ cudaError_t launch_norm(const NormArgs& a, int T, int sm_count, cudaStream_t s)
     const int vpt = nvec <= 256 ? 1 : nvec <= 512 ? 2 : nvec <= 1024 ? 4 : 8;
     const int threads = ((nvec + vpt - 1) / vpt + 31) & ~31;
     // narrow rows: as many threads per SM as with wide ones
-    const int ctas = norm_resident(vpt) * (threads >= 128 ? 1 : 128 / threads) * sm_count;
+    int resident = norm_resident(vpt);
+    if (vpt == 1) resident = resident * 256 / threads < 24 ? resident * 256 / threads : 24;
+    const int ctas = resident * sm_count;
     const dim3 grid(T < ctas ? T : ctas), block(threads);
     if (vpt == 1) return launch_pdl(norm_kernel<1>, grid, block, s, a, T);
     if (vpt == 2) return launch_pdl(norm_kernel<2>, grid, block, s, a, T);
@@ -814,7 +816,7 @@ cudaError_t launch_norm_bwd(const NormBwdArgs& b, float* dw_pre, float* dw_post,
     if (grid > 0) {
         cudaError_t e;
         const bool token = b.f.gate && b.f.per_token;
-        if (H >= 2048 && H <= 8192) {
+        if (H > 2048 && H <= 8192) {
             const int ring = kRows * 4 * 2 * H, weights = 8 * H;
             const int vecs = H <= 4096 ? 1 : 2;
             const int threads = 2 * (((nvec + vecs - 1) / vecs + 31) & ~31);
@@ -832,9 +834,9 @@ cudaError_t launch_norm_bwd(const NormBwdArgs& b, float* dw_pre, float* dw_post,
             // of threads as fit
             const int vpt = nvec <= 2 * kBwdThreads ? 2 : 4;
             const int width = ((nvec + vpt - 1) / vpt + 31) & ~31;
-            int groups = 1;
             // a batch's rows are about 130 KB at most: narrow rows come more at a time
-            const int batch = H > 8192 ? 4 : kMaxBatch;
+            const int batch = H > 8192 ? 4 : H > 1024 ? 8 : kMaxBatch;
+            int groups = 1;
             while (groups < batch && groups * 2 * width <= kBwdThreads) groups *= 2;
             const int smem = 8 * H * groups;
             e = vpt == 2 ? launch_smem(norm_bwd_kernel<2>, grid, kBwdThreads, smem, s, b, batch, groups)
