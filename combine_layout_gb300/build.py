@@ -1,7 +1,8 @@
-"""Build libmoeep.so in-tree for sm_103a with nvcc (no cmake).
+"""Build libmoeep.so in-tree for sm_103a with nvcc (no cmake), and _marshal.so, the
+binding's argument marshalling (csrc/marshal.c), with the C compiler.
 
 Each .cu under csrc/ compiles to an object in parallel, then nvcc links the
-shared library next to this file.  Rebuilds only when a source or header is
+shared library next to this file; _marshal.so is linked against it there.  Rebuilds only when a source or header is
 newer than the library.
 """
 from __future__ import annotations
@@ -11,6 +12,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -18,6 +20,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoeep.so")
+MARSHAL = os.path.join(HERE, "_marshal.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -36,14 +39,14 @@ def _sources():
 
 
 def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h")) \
+    return _sources() + glob.glob(os.path.join(CSRC, "*.c")) + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h")) \
         + [os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(MARSHAL):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(MARSHAL))
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -72,6 +75,14 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CC") or shutil.which("gcc") or "cc", "-O2", "-std=c11", "-shared", "-fPIC", "-I", INCLUDE,
+           "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "marshal.c"), "-o", tmp,
+           "-L", HERE, "-l:libmoeep.so", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"C compiler failed for marshal.c:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MARSHAL)
     return LIB
 
 

@@ -1,4 +1,5 @@
-"""Thin Python binding of libmoeep (ctypes): argument marshalling only.
+"""Thin Python binding of libmoeep (ctypes, and _marshal for the expert block's calls):
+argument marshalling only.
 
 Every function has the name of the C entry point it calls (include/moe_ep.h)
 and takes torch CUDA tensors (or None for NULL).  All work runs in the CUDA
@@ -90,6 +91,7 @@ def _load() -> ctypes.CDLL:
 
 
 _lib = _load()
+from . import _marshal  # noqa: E402  (linked against the library loaded above)
 
 
 def declared_symbols() -> list[str]:
@@ -124,9 +126,9 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
-# Experts and hidden of each live group and handle: what the tensors of the
-# expert block's calls are checked against.
-_sizes: dict[int, tuple[int, int]] = {}
+# Experts, hidden and the norms' workspace of each live group and handle: what the
+# tensors of the expert block's calls are checked against.
+_sizes: dict[int, tuple[int, int, int]] = {}
 
 
 # ------------------------------------------------------------------ entry points
@@ -134,7 +136,7 @@ def moe_ep_create_group(mode: int, experts: int, ranks: int, max_tokens: int, hi
     out = ctypes.c_void_p()
     _check("moe_ep_create_group",
            _lib.moe_ep_create_group(ctypes.byref(out), mode, experts, ranks, max_tokens, hidden))
-    _sizes[out.value] = (experts, hidden)
+    _sizes[out.value] = (experts, hidden, moe_ep_norm_work_floats(out.value))
     return out.value
 
 
@@ -303,68 +305,25 @@ def moe_ep_combine_dedup(handle: int, y, topk_w, drecv_src, partial, out,
                                      drecv_rows, _stream(stream)))
 
 
-# The expert block's calls are made per layer and step, often on a handful of
-# tokens, so their argument checks are kept short: one comparison of type and
-# shape per tensor, addresses passed as plain integers.
-_BF16, _F32 = torch.bfloat16, torch.float32
-
-
-def _wrong(name, t, dtype, shape):
-    want = "x".join("*" if n is None else str(n) for n in shape)
-    return ValueError(f"{name}: expected {dtype} {want}, got {t.dtype} {tuple(t.shape)}"
-                      + ("" if t.is_contiguous() else ", not contiguous"))
-
-
-def _row_tensor(name, t, width):
-    """Address and rows of a contiguous bf16 [rows][width] tensor."""
-    n, w = t.shape
-    if w != width or t.dtype is not _BF16 or not t.is_contiguous():
-        raise _wrong(name, t, _BF16, (None, width))
-    return t.data_ptr(), n
-
-
-def _tensor(name, t, dtype, shape):
-    """Address of a contiguous tensor of this type and shape."""
-    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
-        raise _wrong(name, t, dtype, shape)
-    return t.data_ptr()
-
-
-def _raw_stream(stream) -> int:
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-
-
-def _rows(recv_rows, *held) -> int:
-    """Receive rows that every given row tensor holds."""
-    n = min(held)
-    return n if recv_rows is None else min(int(recv_rows), n)
+# The expert block's calls are marshalled in C (csrc/marshal.c): they are made per
+# layer and step, often on a handful of tokens, and take many tensors each.
+_marshal.setup(torch.bfloat16, torch.float32, torch._C._cuda_getDevice,
+               torch._C._cuda_getCurrentRawStream)
 
 
 def moe_ep_ffn_gate_up(handle: int, x, w_gate_up, hid, gate_up=None, act: int = MOE_EP_ACT_SILU,
                        recv_rows: int | None = None, stream=None) -> None:
     """x [rows][H], w_gate_up [E][2F][H], hid [rows][F], gate_up [rows][2F] or None."""
-    E, H = _sizes[handle]
-    F = hid.shape[1]
-    hid_p, n = _row_tensor("hid", hid, F)
-    x_p, nx = _row_tensor("x", x, H)
-    gu_p, ng = (None, n) if gate_up is None else _row_tensor("gate_up", gate_up, 2 * F)
-    st = _lib.moe_ep_ffn_gate_up(handle, x_p, _tensor("w_gate_up", w_gate_up, _BF16, (E, 2 * F, H)),
-                                 F, act, hid_p, gu_p, _rows(recv_rows, n, nx, ng),
-                                 _raw_stream(stream))
+    E, H, _ = _sizes[handle]
+    st = _marshal.ffn_gate_up(handle, E, H, x, w_gate_up, hid, gate_up, act, recv_rows, stream)
     if st:
         raise MoeEpError("moe_ep_ffn_gate_up", st)
 
 
 def moe_ep_ffn_down(handle: int, hid, w_down, y, recv_rows: int | None = None, stream=None) -> None:
     """hid [rows][F], w_down [E][H][F], y [rows][H]."""
-    E, H = _sizes[handle]
-    F = hid.shape[1]
-    hid_p, n = _row_tensor("hid", hid, F)
-    y_p, ny = _row_tensor("y", y, H)
-    st = _lib.moe_ep_ffn_down(handle, hid_p, _tensor("w_down", w_down, _BF16, (E, H, F)), F, y_p,
-                              _rows(recv_rows, n, ny), _raw_stream(stream))
+    E, H, _ = _sizes[handle]
+    st = _marshal.ffn_down(handle, E, H, hid, w_down, y, recv_rows, stream)
     if st:
         raise MoeEpError("moe_ep_ffn_down", st)
 
@@ -373,15 +332,9 @@ def moe_ep_ffn_down_backward(handle: int, dy, w_down, gate_up, d_gate_up, hid=No
                              act: int = MOE_EP_ACT_SILU, recv_rows: int | None = None,
                              stream=None) -> None:
     """dy [rows][H], w_down [E][H][F], gate_up and d_gate_up [rows][2F], hid [rows][F] or None."""
-    E, H = _sizes[handle]
-    F = w_down.shape[2]
-    dy_p, n = _row_tensor("dy", dy, H)
-    gu_p, ng = _row_tensor("gate_up", gate_up, 2 * F)
-    dgu_p, nd = _row_tensor("d_gate_up", d_gate_up, 2 * F)
-    hid_p, nh = (None, n) if hid is None else _row_tensor("hid", hid, F)
-    st = _lib.moe_ep_ffn_down_backward(handle, dy_p, _tensor("w_down", w_down, _BF16, (E, H, F)),
-                                       gu_p, F, act, dgu_p, hid_p, _rows(recv_rows, n, ng, nd, nh),
-                                       _raw_stream(stream))
+    E, H, _ = _sizes[handle]
+    st = _marshal.ffn_down_backward(handle, E, H, dy, w_down, gate_up, d_gate_up, hid, act,
+                                    recv_rows, stream)
     if st:
         raise MoeEpError("moe_ep_ffn_down_backward", st)
 
@@ -389,16 +342,8 @@ def moe_ep_ffn_down_backward(handle: int, dy, w_down, gate_up, d_gate_up, hid=No
 def moe_ep_ffn_gate_up_backward(handle: int, d_gate_up, w_gate_up, dx,
                                 recv_rows: int | None = None, stream=None) -> None:
     """d_gate_up [rows][2F], w_gate_up [E][2F][H], dx [rows][H]."""
-    E, H = _sizes[handle]
-    F2 = d_gate_up.shape[1]
-    if F2 % 2:
-        raise ValueError("d_gate_up: gate and up columns expected")
-    dgu_p, n = _row_tensor("d_gate_up", d_gate_up, F2)
-    dx_p, nx = _row_tensor("dx", dx, H)
-    st = _lib.moe_ep_ffn_gate_up_backward(handle, dgu_p,
-                                          _tensor("w_gate_up", w_gate_up, _BF16, (E, F2, H)),
-                                          F2 // 2, dx_p, _rows(recv_rows, n, nx),
-                                          _raw_stream(stream))
+    E, H, _ = _sizes[handle]
+    st = _marshal.ffn_gate_up_backward(handle, E, H, d_gate_up, w_gate_up, dx, recv_rows, stream)
     if st:
         raise MoeEpError("moe_ep_ffn_gate_up_backward", st)
 
@@ -406,13 +351,7 @@ def moe_ep_ffn_gate_up_backward(handle: int, d_gate_up, w_gate_up, dx,
 def moe_ep_ffn_weight_grad(handle: int, a, b, dw, accumulate: bool = False,
                            recv_rows: int | None = None, stream=None) -> None:
     """a [rows][m], b [rows][n] bf16, dw [E][m][n] bf16 or fp32."""
-    m, n = a.shape[1], b.shape[1]
-    a_p, na = _row_tensor("a", a, m)
-    b_p, nb = _row_tensor("b", b, n)
-    f32 = dw.dtype is _F32
-    dw_p = _tensor("dw", dw, _F32 if f32 else _BF16, (_sizes[handle][0], m, n))
-    st = _lib.moe_ep_ffn_weight_grad(handle, a_p, m, b_p, n, dw_p, int(f32), int(bool(accumulate)),
-                                     _rows(recv_rows, na, nb), _raw_stream(stream))
+    st = _marshal.ffn_weight_grad(handle, _sizes[handle][0], a, b, dw, accumulate, recv_rows, stream)
     if st:
         raise MoeEpError("moe_ep_ffn_weight_grad", st)
 
@@ -420,50 +359,20 @@ def moe_ep_ffn_weight_grad(handle: int, a, b, dw, accumulate: bool = False,
 def moe_ep_combine_backward(handle: int, dout, y, topk_w, dy, dw, recv_rows: int | None = None,
                             stream=None) -> None:
     """dout [T][H], y and dy [rows][H] bf16, topk_w and dw [T][k] fp32."""
-    H = _sizes[handle][1]
-    y_p, n = _row_tensor("y", y, H)
-    dy_p, nd = _row_tensor("dy", dy, H)
-    pairs = topk_w.shape
-    st = _lib.moe_ep_combine_backward(handle, _row_tensor("dout", dout, H)[0], y_p,
-                                      _tensor("topk_w", topk_w, _F32, pairs), dy_p,
-                                      _tensor("dw", dw, _F32, pairs), _rows(recv_rows, n, nd),
-                                      _raw_stream(stream))
+    st = _marshal.combine_backward(handle, _sizes[handle][1], dout, y, topk_w, dy, dw, recv_rows,
+                                   stream)
     if st:
         raise MoeEpError("moe_ep_combine_backward", st)
-
-
-def _token_tensor(name, t, T, H):
-    """Address of a contiguous bf16 tensor with at least T rows of H, or None."""
-    if t is None:
-        return None
-    p, n = _row_tensor(name, t, H)
-    if n < T:
-        raise _wrong(name, t, _BF16, (T, H))
-    return p
-
-
-def _channels(name, t, n):
-    """Address of at least n contiguous fp32 values, or None."""
-    if t is None:
-        return None
-    if t.dtype is not _F32 or t.numel() < n or not t.is_contiguous():
-        raise _wrong(name, t, _F32, (n,))
-    return t.data_ptr()
 
 
 def moe_ep_norm_residual(group: int, o, res, w_post, gate, w_pre, res_out, y,
                          res_scale: float = 1.0, gate_per_token: bool = False, eps: float = 1e-6,
                          num_tokens: int | None = None, stream=None) -> None:
     """o, res, res_out, y [T][H] bf16, w_post, w_pre [H] and gate [H] or [T] fp32; None for absent."""
-    H = _sizes[group][1]
-    first = res if o is None else o
-    T = num_tokens if num_tokens is not None else 0 if first is None else first.shape[0]
-    st = _lib.moe_ep_norm_residual(group, _token_tensor("o", o, T, H),
-                                   _token_tensor("res", res, T, H), _channels("w_post", w_post, H),
-                                   _channels("gate", gate, T if gate_per_token else H),
-                                   1 if gate_per_token else 0, _channels("w_pre", w_pre, H),
-                                   res_scale, eps, T, _token_tensor("res_out", res_out, T, H),
-                                   _token_tensor("y", y, T, H), _raw_stream(stream))
+    if num_tokens is None:
+        num_tokens = o.shape[0] if o is not None else res.shape[0] if res is not None else 0
+    st = _marshal.norm_residual(group, _sizes[group][1], num_tokens, o, res, w_post, gate,
+                                gate_per_token, w_pre, res_scale, eps, res_out, y, stream)
     if st:
         raise MoeEpError("moe_ep_norm_residual", st)
 
@@ -481,18 +390,12 @@ def moe_ep_norm_residual_backward(group: int, o, res, w_post, gate, w_pre, dr, d
                                   num_tokens: int | None = None, stream=None) -> None:
     """dr, dy, d_o, dres [T][H] bf16, dw_post, dw_pre [H] and dgate (as gate) fp32, work
     [moe_ep_norm_work_floats] fp32; None for absent."""
-    H = _sizes[group][1]
-    first = res if o is None else o
-    T = num_tokens if num_tokens is not None else 0 if first is None else first.shape[0]
-    gates = T if gate_per_token else H
-    st = _lib.moe_ep_norm_residual_backward(
-        group, _token_tensor("o", o, T, H), _token_tensor("res", res, T, H),
-        _channels("w_post", w_post, H), _channels("gate", gate, gates), 1 if gate_per_token else 0,
-        _channels("w_pre", w_pre, H), res_scale, eps, T, _token_tensor("dr", dr, T, H),
-        _token_tensor("dy", dy, T, H), _token_tensor("d_o", d_o, T, H),
-        _token_tensor("dres", dres, T, H), _channels("dw_post", dw_post, H),
-        _channels("dgate", dgate, gates), _channels("dw_pre", dw_pre, H),
-        _channels("work", work, moe_ep_norm_work_floats(group)), _raw_stream(stream))
+    if num_tokens is None:
+        num_tokens = o.shape[0] if o is not None else res.shape[0] if res is not None else 0
+    _, H, floats = _sizes[group]
+    st = _marshal.norm_residual_backward(group, H, num_tokens, floats, o, res, w_post, gate,
+                                         gate_per_token, w_pre, res_scale, eps, dr, dy, d_o, dres,
+                                         dw_post, dgate, dw_pre, work, stream)
     if st:
         raise MoeEpError("moe_ep_norm_residual_backward", st)
 

@@ -37,7 +37,7 @@ def test_null_handles_are_refused(ep):
 
 def test_binding_checks_types_and_shapes(ep, monkeypatch):
     E, H, F, n = 4, 64, 32, 10
-    monkeypatch.setitem(ep._sizes, 1, (E, H))
+    monkeypatch.setitem(ep._sizes, 1, (E, H, 0))
     z = lambda *s, dtype=torch.bfloat16: torch.zeros(s, dtype=dtype)  # noqa: E731
     x, hid, w, wd = z(n, H), z(n, F), z(E, 2 * F, H), z(E, H, F)
     bad = [
