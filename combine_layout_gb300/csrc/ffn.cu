@@ -2,31 +2,38 @@
 // on the fifth-generation tensor cores: products of the rows with their
 // expert's weights, the activation fused into the product that feeds it.
 //
-// Orientation.  A tile is 256 weight rows (features) x up to 256 receive rows
-// of one expert, shared by a pair of CTAs (cta_group::2): the weights are the
-// tensor core's fixed operand of 2 x 128 rows and the tokens its n dimension,
-// which any multiple of 32 up to 256 serves.  An
-// expert's share of a batch is ragged and often small (a decoding step gives
-// an expert a handful of rows), so the ragged dimension goes where the
-// instruction takes it; with tokens on the 128-row side an expert with 5 rows
-// would cost as much as one with 128.  The pair halves what a CTA stages of the tokens: 32 KB for
-// 128 x 256 x 64 products per CTA where a CTA alone stages 48 KB.
+// Orientation.  A tile is 256 weight rows (features) x up to 256 receive rows of
+// one expert, shared by a pair of CTAs (cta_group::2): the weights are the tensor
+// core's fixed operand of 2 x 128 rows and the tokens its n dimension, which any
+// multiple of 32 up to 256 serves.  An expert's share of a batch is ragged and
+// often small (a decoding step gives an expert a handful of rows), so the ragged
+// dimension goes where the instruction takes it; with tokens on the 128-row side
+// an expert with 5 rows would cost as much as one with 128.  The pair halves what
+// a CTA stages of the tokens: 32 KB for 128 x 256 x 64 products per CTA, where a
+// CTA alone stages 48 KB (32768 rows x 7168 x 2048, forward: 2276 us alone, 1878
+// in pairs).
 //
 // Roles of a CTA (320 threads): one thread loads its operand tiles by TMA into a
 // ring of shared-memory stages, one thread of the pair's first CTA issues the
 // products, eight warps read the fp32 accumulators from tensor memory, apply the
-// activation and store bf16.  The accumulators are double-buffered, so a tile's epilogue runs
-// under the next tile's products.  CTAs are persistent; the tile list is
-// derived on the device from the layout's counts (no host synchronisation).
+// activation and store bf16.  The accumulators are double-buffered, so a tile's
+// epilogue runs under the next tile's products.  CTAs are persistent; the tile
+// list is derived on the device from the layout's counts (no host
+// synchronisation).
 //
 // Epilogue.  The accumulators hold features along tensor memory's lanes, the
 // outputs along a row.  They are read as 8 x 8 fragments, rounded in pairs and
 // transposed on the way through a warp's own piece of shared memory
-// (stmatrix.trans), from where 16-byte vectors go to the rows; the backward
-// pass's gate and up values come in the same way (ldmatrix.trans).
-// Storing each lane's values directly, two bytes at a time, took some 24
-// instructions a column and bound the kernels (8 experts x 512 rows x 4096 x
-// 2048, down: 58 us; the products alone need 36).
+// (stmatrix.trans), from where 16-byte vectors go to the rows; the backward pass's
+// gate and up values come in the same way (ldmatrix.trans).  Storing each lane's
+// values directly, two bytes at a time, took some 24 instructions a column and
+// bound the kernels (8 experts x 512 rows x 4096 x 2048, gate and up: 150 us
+// against 91).
+//
+// What bounds it: with few rows an expert the weights (256 experts x 7168 x 2048,
+// 4 rows each: 7.06 TB/s); with many the tensor cores (32 experts x 512 rows x
+// 4096 x 2048: gate and up 1.72 PFLOP/s, 1.6 with 512 +- 20 rows, whose tiles are
+// two of 256 or three of 192 columns), and in long runs the power limit (1.4).
 #include <cuda_bf16.h>
 
 #include "common.cuh"

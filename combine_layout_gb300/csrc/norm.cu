@@ -112,7 +112,10 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float (*part)[32])
 // Forward: a CTA takes tokens in grid-stride order, a token's row in registers
 // (VPT vectors per thread), and loads the next token's row as soon as this one's
 // has been combined into r, so loads are in flight through both sums' latency.
-// The weights come from L1.
+// The weights come from L1.  16384 x 7168: 158.5 us, 5.93 TB/s; bound by HBM but
+// for the sums' latency, of which more CTAs would hide more: registers allow three
+// of 224 threads at H = 7168 (with four the row spills: 204 us), ten of 128 at
+// 1024 (25.7 us for 16384 tokens, 36 with four).
 constexpr int norm_resident(int vpt) { return vpt == 1 ? 5 : vpt == 2 ? 4 : vpt == 4 ? 3 : 1; }  // CTAs per SM
 
 template <int VPT>
@@ -525,7 +528,8 @@ __global__ void __launch_bounds__(kRowVecs == 2 && WS ? 896 : 1024, 1) norm_bwd_
 // at a time, in three passes: mean(o^2), the other sums -- both with the 16 warps
 // spread over the batch's rows -- and then the outputs, with a thread on the same
 // vectors of every row.  Narrow rows need few threads each, so the sums of many
-// rows share a barrier (16384 x 1024: 72 us, 81 with a barrier per row); rows
+// rows share a barrier (16384 x 1024: 69 us, 81 with a barrier per row; 16384 x
+// 2048: 124 us, 154 with one per row); rows
 // wider than 8192 do not fit the ring.  At 4096 x 7168 the later passes' reads
 // from L2 are what it waits for (129 us).
 constexpr int kMaxBatch = 16;  // tokens at a time: one warp to a row at least
@@ -835,6 +839,7 @@ cudaError_t launch_norm_bwd(const NormBwdArgs& b, float* dw_pre, float* dw_post,
             const int vpt = nvec <= 2 * kBwdThreads ? 2 : 4;
             const int width = ((nvec + vpt - 1) / vpt + 31) & ~31;
             // a batch's rows are about 130 KB at most: narrow rows come more at a time
+            // (16384 x 2048: 124 us by 8, 137 by 16; 1024: 75 by 8, 69 by 16)
             const int batch = H > 8192 ? 4 : H > 1024 ? 8 : kMaxBatch;
             int groups = 1;
             while (groups < batch && groups * 2 * width <= kBwdThreads) groups *= 2;

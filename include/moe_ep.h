@@ -513,7 +513,9 @@ MOE_EP_API int moe_ep_combine_backward(moe_ep_handle_t h, const void* dout, cons
  * res_out, y     device bf16 [num_tokens][H]; either may be NULL, not both.  An
  *         output may be the same buffer as o or res, but not overlap one
  *         otherwise.
- * eps must not be negative.  Any num_tokens >= 0.  Asynchronous on `stream`. */
+ * eps must not be negative.  Any num_tokens >= 0.  Tensors and fp32 arrays of H
+ * values are 16-byte aligned.  Asynchronous on `stream`.  Errors:
+ * MOE_EP_ERR_INVALID. */
 MOE_EP_API int moe_ep_norm_residual(moe_ep_group_t g, const void* o, const void* res,
                                     const float* w_post, const float* gate, int gate_per_token,
                                     const float* w_pre, float res_scale, float eps, int num_tokens,
