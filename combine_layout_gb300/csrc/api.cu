@@ -1129,6 +1129,14 @@ int moe_ep_ffn_weight_grad(moe_ep_handle_t h, const void* a, int m, const void* 
     return cuda_status(launch_weight_grad(a, b, recv_rows, fp32, ga, h->g->sm_count, s));
 }
 
+int moe_ep_get_routed(moe_ep_handle_t h, int* num_tokens, int* topk)
+{
+    if (!h || !num_tokens || !topk || !h->routed) return MOE_EP_ERR_INVALID;
+    *num_tokens = h->T;
+    *topk = h->k;
+    return MOE_EP_OK;
+}
+
 int moe_ep_combine_backward(moe_ep_handle_t h, const void* dout, const void* y, const float* topk_w,
                             void* dy, float* dw, int64_t recv_rows, moe_ep_stream_t stream)
 {

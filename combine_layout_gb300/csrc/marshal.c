@@ -39,6 +39,16 @@ static int64_t integer(PyObject* o, int* bad)
     return v;
 }
 
+static int small(PyObject* o, const char* name, int* bad)
+{
+    const int64_t v = integer(o, bad);
+    if (!*bad && (v < INT32_MIN || v > INT32_MAX)) {
+        PyErr_Format(PyExc_ValueError, "%s: %lld is out of range", name, (long long)v);
+        *bad = 1;
+    }
+    return *bad ? 0 : (int)v;
+}
+
 static void* pointer(PyObject* o, int* bad)
 {
     void* p = o == Py_None ? NULL : PyLong_AsVoidPtr(o);
@@ -182,7 +192,7 @@ CALL(ffn_gate_up, 10)
     void* x = rows_of(a[3], "x", H, &n, 0, &bad);
     void* w = tensor(a[4], "w_gate_up", t_bf16, 3, wd, 0, &bad);
     void* gu = rows_of(a[6], "gate_up", 2 * F, &n, 1, &bad);
-    const int act = (int)integer(a[7], &bad);
+    const int act = small(a[7], "act", &bad);
     moe_ep_stream_t s = stream_of(a[9], &bad);
 RETURN(moe_ep_ffn_gate_up(h, x, w, (int)F, act, hid, gu, n, s))
 
@@ -210,7 +220,7 @@ CALL(ffn_down_backward, 11)
     void* gu = rows_of(a[5], "gate_up", 2 * F, &n, 0, &bad);
     void* dgu = rows_of(a[6], "d_gate_up", 2 * F, &n, 0, &bad);
     void* hid = rows_of(a[7], "hid", F, &n, 1, &bad);
-    const int act = (int)integer(a[8], &bad);
+    const int act = small(a[8], "act", &bad);
     moe_ep_stream_t s = stream_of(a[10], &bad);
 RETURN(moe_ep_ffn_down_backward(h, dy, w, gu, (int)F, act, dgu, hid, n, s))
 
@@ -259,12 +269,19 @@ CALL(combine_backward, 9)
     void* dy = rows_of(a[5], "dy", H, &n, 0, &bad);
     void* dw = tensor(a[6], "dw", t_f32, 2, pairs, 0, &bad);
     moe_ep_stream_t s = stream_of(a[8], &bad);
+    int T = 0, k = 0;
+    if (!bad && moe_ep_get_routed(h, &T, &k) == MOE_EP_OK && (od[0] < T || pairs[0] < T || (T && pairs[1] != k))) {
+        PyErr_Format(PyExc_ValueError, "dout, topk_w: %lld and %lld tokens, k = %lld; routed %d, k = %d",
+                     (long long)od[0], (long long)pairs[0], (long long)pairs[1], T, k);
+        bad = 1;
+    }
 RETURN(moe_ep_combine_backward(h, dout, y, w, dy, dw, n, s))
 
 /* group, H, T, o, res, w_post, gate, gate_per_token, w_pre, res_scale, eps, res_out, y, stream */
 CALL(norm_residual, 14)
     moe_ep_group_t g = pointer(a[0], &bad);
-    const int64_t H = integer(a[1], &bad), T = integer(a[2], &bad);
+    const int64_t H = integer(a[1], &bad);
+    const int T = small(a[2], "num_tokens", &bad);
     const int per_token = truth(a[7], &bad);
     void* o = tokens_of(a[3], "o", T, H, &bad);
     void* res = tokens_of(a[4], "res", T, H, &bad);
@@ -275,13 +292,14 @@ CALL(norm_residual, 14)
     void* out = tokens_of(a[11], "res_out", T, H, &bad);
     void* y = tokens_of(a[12], "y", T, H, &bad);
     moe_ep_stream_t s = stream_of(a[13], &bad);
-RETURN(moe_ep_norm_residual(g, o, res, w_post, gate, per_token, w_pre, scale, eps, (int)T, out, y, s))
+RETURN(moe_ep_norm_residual(g, o, res, w_post, gate, per_token, w_pre, scale, eps, T, out, y, s))
 
 /* group, H, T, work floats, o, res, w_post, gate, gate_per_token, w_pre, res_scale, eps, dr, dy, d_o, dres,
  * dw_post, dgate, dw_pre, work, stream */
 CALL(norm_residual_backward, 21)
     moe_ep_group_t g = pointer(a[0], &bad);
-    const int64_t H = integer(a[1], &bad), T = integer(a[2], &bad), floats = integer(a[3], &bad);
+    const int64_t H = integer(a[1], &bad), floats = integer(a[3], &bad);
+    const int T = small(a[2], "num_tokens", &bad);
     const int per_token = truth(a[8], &bad);
     const int64_t gates = per_token ? T : H;
     void* o = tokens_of(a[4], "o", T, H, &bad);
@@ -299,7 +317,7 @@ CALL(norm_residual_backward, 21)
     float* dw_pre = values_of(a[18], "dw_pre", H, 1, &bad);
     float* work = values_of(a[19], "work", floats, 0, &bad);
     moe_ep_stream_t s = stream_of(a[20], &bad);
-RETURN(moe_ep_norm_residual_backward(g, o, res, w_post, gate, per_token, w_pre, scale, eps, (int)T, dr, dy, d_o, dres,
+RETURN(moe_ep_norm_residual_backward(g, o, res, w_post, gate, per_token, w_pre, scale, eps, T, dr, dy, d_o, dres,
                                      dw_post, dgate, dw_pre, work, s))
 
 #define METHOD(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, NULL}

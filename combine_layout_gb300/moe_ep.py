@@ -76,6 +76,7 @@ def _load() -> ctypes.CDLL:
         "moe_ep_ffn_down_backward": [P, P, P, P, I, I, P, P, I64, P],
         "moe_ep_ffn_gate_up_backward": [P, P, P, I, P, I64, P],
         "moe_ep_ffn_weight_grad": [P, P, I, P, I, P, I, I, I64, P],
+        "moe_ep_get_routed": [P, ctypes.POINTER(I), ctypes.POINTER(I)],
         "moe_ep_combine_backward": [P, P, P, P, P, P, I64, P],
         "moe_ep_norm_residual": [P, P, P, P, P, I, P, F, F, I, P, P, P],
         "moe_ep_norm_work_floats": [P, ctypes.POINTER(ctypes.c_int64)],
@@ -354,6 +355,14 @@ def moe_ep_ffn_weight_grad(handle: int, a, b, dw, accumulate: bool = False,
     st = _marshal.ffn_weight_grad(handle, _sizes[handle][0], a, b, dw, accumulate, recv_rows, stream)
     if st:
         raise MoeEpError("moe_ep_ffn_weight_grad", st)
+
+
+def moe_ep_get_routed(handle: int) -> tuple[int, int]:
+    """Returns (num_tokens, topk) of the handle's last route."""
+    tokens, topk = ctypes.c_int(), ctypes.c_int()
+    _check("moe_ep_get_routed", _lib.moe_ep_get_routed(ctypes.c_void_p(handle), ctypes.byref(tokens),
+                                                       ctypes.byref(topk)))
+    return tokens.value, topk.value
 
 
 def moe_ep_combine_backward(handle: int, dout, y, topk_w, dy, dw, recv_rows: int | None = None,

@@ -486,6 +486,10 @@ MOE_EP_API int moe_ep_ffn_weight_grad(moe_ep_handle_t h, const void* a, int m, c
                                       void* dw, int fp32, int accumulate, int64_t recv_rows,
                                       moe_ep_stream_t stream);
 
+/* Tokens and choices of the handle's last moe_ep_route: what a binding checks its
+ * tensors' sizes against.  MOE_EP_ERR_INVALID before the first one. */
+MOE_EP_API int moe_ep_get_routed(moe_ep_handle_t h, int* num_tokens, int* topk);
+
 /* Backward of moe_ep_combine: for every pair with a row
  *   dy[row(t, j)] = bf16_rn(topk_w[t][j] * dout[t]),
  *   dw[t][j] = sum over h of dout[t][h] * y[row(t, j)][h]   (fp32),

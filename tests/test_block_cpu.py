@@ -58,3 +58,22 @@ def test_binding_checks_types_and_shapes(ep, monkeypatch):
     for f in bad:
         with pytest.raises(ValueError):
             f()
+
+
+def test_numbers_that_do_not_fit_are_refused(ep, monkeypatch):
+    H, n = 64, 10
+    monkeypatch.setitem(ep._sizes, 1, (4, H, 0))
+    z = lambda *s, dtype=torch.bfloat16: torch.zeros(s, dtype=dtype)  # noqa: E731
+    x, far = z(n, H), -2**32 + 5                     # 5 in 32 bits
+    for f in (lambda: ep.moe_ep_norm_residual(1, x, None, None, None, None, x, None, num_tokens=far),
+              lambda: ep.moe_ep_norm_residual_backward(1, x, None, None, None, None, x, None, x, None, None, None,
+                                                       None, z(1, dtype=torch.float32)[:0], num_tokens=far),
+              lambda: ep.moe_ep_ffn_gate_up(1, x, z(4, 64, H), z(n, 32), act=2**32),
+              lambda: ep.moe_ep_ffn_down_backward(1, x, z(4, H, 32), z(n, 64), z(n, 64), act=2**32)):
+        with pytest.raises(ValueError, match="out of range"):
+            f()
+
+
+def test_routed_sizes_of_a_null_handle(ep):
+    a, b = ctypes.c_int(), ctypes.c_int()
+    assert ep._lib.moe_ep_get_routed(None, ctypes.byref(a), ctypes.byref(b)) == INVALID

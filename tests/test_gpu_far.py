@@ -134,3 +134,23 @@ def test_addresses_off_16_bytes_are_refused():
         assert e.value.status == ep.MOE_EP_ERR_INVALID
     ep.moe_ep_destroy_handle(h)
     ep.moe_ep_destroy_group(g)
+
+
+def test_combine_backward_refuses_other_tokens_than_routed():
+    ep = _ep()
+    g = ep.moe_ep_create_group(1, 2, 1, 4, 64)
+    h = ep.moe_ep_create_handle(g, 2)
+    with pytest.raises(ep.MoeEpError):
+        ep.moe_ep_get_routed(h)
+    ep.moe_ep_route(h, None, 4, 2, torch.tensor([[0, 1]] * 4, dtype=torch.int32, device=DEV))
+    assert ep.moe_ep_get_routed(h) == (4, 2)
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device=DEV)  # noqa: E731
+    f32 = lambda *s: torch.zeros(s, device=DEV)  # noqa: E731
+    for dout, w, dw in ((bf(3, 64), f32(4, 2), f32(4, 2)), (bf(4, 64), f32(3, 2), f32(3, 2)),
+                        (bf(4, 64), f32(4, 1), f32(4, 1)), (bf(4, 64), f32(4, 3), f32(4, 3))):
+        with pytest.raises(ValueError, match="routed"):
+            ep.moe_ep_combine_backward(h, dout, bf(8, 64), w, bf(8, 64), dw)
+    ep.moe_ep_combine_backward(h, bf(5, 64), bf(8, 64), f32(6, 2), bf(8, 64), f32(6, 2))  # longer ones serve
+    torch.cuda.synchronize()
+    ep.moe_ep_destroy_handle(h)
+    ep.moe_ep_destroy_group(g)
