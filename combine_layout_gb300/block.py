@@ -24,7 +24,9 @@ class MoeBlock:
     """Weights: w_gate_up [E][2F][H] and w_down [E][H][F] bf16; w_in, w_post (or
     None), w_next [H] and gate ([H], [T] with gate_per_token, or None) fp32.
     The pipeline is a bf16 one; with ``training`` the forward pass keeps what
-    ``backward`` needs."""
+    ``backward`` needs: its own buffers and the pipeline's (the receive rows, the
+    combined rows, the routing), so no other block uses that pipeline between a
+    forward pass and its backward pass.  Streams are torch.cuda streams or None."""
 
     def __init__(self, pipe: EpPipeline, w_gate_up, w_down, w_in, w_post, w_next, gate=None,
                  gate_per_token: bool = False, res_scale: float = 1.0, act: int = ep.MOE_EP_ACT_SILU,
@@ -71,7 +73,7 @@ class MoeBlock:
         """Gradients of (h', x_next) -> the gradient of h; those of the weights
         are left in dw_* and dgate, that of the gate weights in d_topk_w.  The
         experts' weight gradients are fp32 and, with ``accumulate``, added up
-        over calls.  d_x_router(d_topk_w) gives the router's share of x's
+        over calls.  d_x_router(d_topk_w), on ``stream``, gives the router's share of x's
         gradient, bf16 [T][H], or None when the router is not trained."""
         if not self.training:
             raise ValueError("the block was not made for training")
